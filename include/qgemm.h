@@ -68,6 +68,7 @@ typedef enum { QGEMM_F16 = 0, QGEMM_BF16 = 1 } qgemm_dtype;
 #define QGEMM_DEV_BAD_SCHEDULE 1   /* d_bits/d_offs inconsistent or not matching qw_rows */
 #define QGEMM_DEV_BAD_PERM 2       /* a perm entry outside [0, K)                        */
 #define QGEMM_DEV_TIMEOUT 4        /* a pipeline wait gave up after ~1 s                 */
+#define QGEMM_DEV_BAD_PAGE 8       /* a token without a valid page in the block table    */
 
 /* ---------------------------------------------------------------- host only */
 
@@ -220,6 +221,98 @@ int qgemm_kv_quantize(const uint16_t* d_v, int64_t nvec, int D, int bits, uint32
                       uint16_t* d_scales, void* stream);
 int qgemm_kv_dequantize(const uint32_t* d_codes, const uint16_t* d_scales, int64_t nvec, int D, int bits,
                         uint16_t* d_v, void* stream);
+
+/* Paged KV cache in the same codes (rotated vectors, groups of 32, widths 2, 3,
+ * 4, 5, 6 or 8, K and V each its own): where qgemm_kv_quantize turns one array
+ * into codes, these three keep a serving batch's K and V in pages, write new
+ * tokens, read tokens back and attend over the pages without ever expanding
+ * them (navi2ai ExLlamaV3 page, "核心能力": 2-8 bit caches; paging and the
+ * record layout are this library's own).
+ *
+ * A cache is num_pages pages of page_size tokens (32, 64, 128, ... 4096).  A
+ * page holds kv_heads * page_size / 32 records, [kv_heads][page_size / 32], of
+ * 4 D (k_bits + v_bits + 1) bytes each: 32 tokens of one head, K codes (4 D
+ * k_bits bytes), K scales (D fp16), V codes, V scales.  With G = D / 32, codes
+ * are 32 streams of D b / 8 bytes made of units of 8 codes = b bytes, little
+ * endian, slot i at bits [b i, b i + b); streams are stored in chunks of C
+ * bytes (the largest of 16, 8, 4 that divides D b / 16), chunk c of stream l at
+ * (32 c + l) C:
+ *   K: token 8 tt + r, dim 32 g + 8 j + i in stream 4 r + j, unit tt G + g,
+ *      slot i (b <= 4); for b >= 5 the slots hold i = 0,1,4,5,2,3,6,7;
+ *      its scale at [r][tt][g];
+ *   V: token 8 tt + 2 j + u, dim 64 h + 32 e + 4 r + i in stream 4 r + j, unit
+ *      (2 tt + u) D/64 + h, slot 4 e + i; its scale at [j][g][tt][u].
+ * The codes and scales of a token are those qgemm_kv_quantize gives, bit for
+ * bit.  Slots that no token was written to may hold anything, NaN scales too. */
+typedef struct {
+    uint32_t* d_pages;  /* [num_pages] x qgemm_kv_page_words() words, 128-byte aligned */
+    int64_t num_pages;  /* 1 .. 2^31 - 1                                               */
+    int32_t page_size;  /* tokens per page: a power of two, 32 .. 4096                 */
+    int32_t kv_heads;   /* 1 .. 1024                                                   */
+    int32_t head_dim;   /* D: 64, 128 or 256                                           */
+    int32_t k_bits, v_bits;
+} qgemm_kv_cache;
+
+/* The batch a call works on.  Sequence b has d_seq_lens[b] tokens, of which the
+ * last n_b = d_cu_new[b + 1] - d_cu_new[b] are new: rows d_cu_new[b] .. of the
+ * call's row operands, at positions seq_len - n_b ...  Position p is slot
+ * p % page_size of page d_block_table[b * table_stride + p / page_size].
+ * d_cu_new starts at 0 and does not fall; n_b may be 0.  Rows from
+ * d_cu_new[num_seqs] on (padding) are neither read nor written.  A row at a
+ * negative position (n_b > seq_len: padded sequences of a captured graph) has
+ * no token: append and gather skip it, attend writes zeros and an lse of -inf.
+ * A position whose table entry lies outside the row or outside [0, num_pages)
+ * sets QGEMM_DEV_BAD_PAGE; it is not written or read, and attend leaves it out
+ * of the sums.  Two sequences may share pages that only hold tokens no call
+ * writes; a slot written twice in one call has no defined content. */
+typedef struct {
+    const int32_t* d_block_table;
+    int64_t table_stride;       /* elements between rows, >= max_pages             */
+    const int32_t* d_seq_lens;  /* [num_seqs]                                      */
+    const int32_t* d_cu_new;    /* [num_seqs + 1]                                  */
+    int32_t num_seqs;           /* 0 .. 65535                                      */
+    int32_t max_pages;          /* entries in a row of the table                   */
+} qgemm_kv_batch;
+
+/* 32-bit words of one page, or a negative qgemm_status.  Host only. */
+int64_t qgemm_kv_page_words(int kv_heads, int head_dim, int k_bits, int v_bits, int page_size);
+
+/* Row operands are [num_rows][heads][D] values of `dtype` (a qgemm_dtype) with
+ * strides in elements; pointers 16-byte aligned, strides multiples of 8;
+ * num_rows at least the last entry of d_cu_new (rows past it are ignored where
+ * d_cu_new names more).
+ * Written operands must not overlap themselves (QGEMM_ERR_SHAPE). */
+
+/* Writes the batch's new tokens into their pages: d_k and d_v [num_rows][kv_heads][D]. */
+int qgemm_kv_append(const qgemm_kv_cache* cache, const qgemm_kv_batch* batch, int num_rows, const void* d_k, int64_t k_row_stride,
+                    int64_t k_head_stride, const void* d_v, int64_t v_row_stride, int64_t v_head_stride, int dtype,
+                    void* stream);
+
+/* Reads the last n_b tokens of every sequence back (n_b = seq_len: all of it):
+ * v' = H_D ((q - 2^(b-1)) s) / D, rounded once to dtype, into d_k and d_v. */
+int qgemm_kv_gather(const qgemm_kv_cache* cache, const qgemm_kv_batch* batch, int num_rows, void* d_k, int64_t k_row_stride,
+                    int64_t k_head_stride, void* d_v, int64_t v_row_stride, int64_t v_head_stride, int dtype,
+                    void* stream);
+
+/* Attention of the new tokens over their sequences in the cache (write them
+ * first): row r of sequence b, at position p, sees positions 0 .. p, and with
+ * window > 0 only the last `window` of them.  Query head h reads KV head
+ * h / (q_heads / kv_heads).
+ *   out = sum_t softmax(scale q . k'_t) v'_t,  lse = ln sum_t exp(scale q . k'_t)
+ * with k', v' the values gather gives before rounding.  A row that sees nothing
+ * gives zeros and -inf.
+ *   d_q, d_out [num_rows][q_heads][D] of `dtype`; q_heads a multiple of kv_heads;
+ *   d_lse      optional fp32 [num_rows][q_heads];
+ *   d_ws       qgemm_kv_attend_workspace_bytes(cache, q_heads) bytes, zero-filled
+ *              before its first use and reusable after each completed call; calls
+ *              that overlap on the GPU must not share it.
+ * The number of tokens and the split over them are read on the device, so a
+ * captured call can be replayed with other lengths. */
+size_t qgemm_kv_attend_workspace_bytes(const qgemm_kv_cache* cache, int q_heads);
+int qgemm_kv_attend(const qgemm_kv_cache* cache, const qgemm_kv_batch* batch, int num_rows, const void* d_q, int64_t q_row_stride,
+                    int64_t q_head_stride, int dtype, int q_heads, float scale, int window, void* d_out,
+                    int64_t out_row_stride, int64_t out_head_stride, float* d_lse, void* d_ws, size_t ws_bytes,
+                    void* stream);
 
 size_t qgemm_quantize_workspace_bytes(int K, int N);
 int qgemm_quantize(const uint16_t* d_w, const uint8_t* d_bits, int K, int N, uint8_t* d_codes,

@@ -11,7 +11,8 @@ Names follow the C entry points: ``qgemm_pack``, ``qgemm_dequant``, ``qgemm``,
 ``qgemm_validate_schedule``, ``qgemm_device_error``, ``qgemm_path_for``,
 ``qgemm_autotune``, ``qgemm_set_autotune``, ``qgemm_tune_lookup``,
 ``qgemm_tune_record``, ``qgemm_tune_clear``, ``qgemm_iqm``, ``qgemm_quantize``,
-``qgemm_kv_quantize``, ``qgemm_kv_dequantize``.
+``qgemm_kv_quantize``, ``qgemm_kv_dequantize``, ``qgemm_kv_page_words``,
+``qgemm_kv_append``, ``qgemm_kv_gather``, ``qgemm_kv_attend``.
 """
 from __future__ import annotations
 
@@ -28,6 +29,18 @@ QGEMM_BF16 = 1
 DEV_BAD_SCHEDULE = 1
 DEV_BAD_PERM = 2
 DEV_TIMEOUT = 4
+DEV_BAD_PAGE = 8
+
+
+class _CacheStruct(ctypes.Structure):
+    _fields_ = [("d_pages", ctypes.c_void_p), ("num_pages", ctypes.c_int64), ("page_size", ctypes.c_int32),
+                ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("k_bits", ctypes.c_int32),
+                ("v_bits", ctypes.c_int32)]
+
+
+class _BatchStruct(ctypes.Structure):
+    _fields_ = [("d_block_table", ctypes.c_void_p), ("table_stride", ctypes.c_int64), ("d_seq_lens", ctypes.c_void_p),
+                ("d_cu_new", ctypes.c_void_p), ("num_seqs", ctypes.c_int32), ("max_pages", ctypes.c_int32)]
 
 
 class QGemmError(RuntimeError):
@@ -66,6 +79,11 @@ def _load():
         "qgemm_quantize": (I, [P, P, I, I, P, P, P, P, P, SZ, P]),
         "qgemm_kv_quantize": (I, [P, I64, I, I, P, P, P]),
         "qgemm_kv_dequantize": (I, [P, P, I64, I, I, P, P]),
+        "qgemm_kv_page_words": (I64, [I, I, I, I, I]),
+        "qgemm_kv_append": (I, [P, P, I, P, I64, I64, P, I64, I64, I, P]),
+        "qgemm_kv_gather": (I, [P, P, I, P, I64, I64, P, I64, I64, I, P]),
+        "qgemm_kv_attend_workspace_bytes": (SZ, [P, I]),
+        "qgemm_kv_attend": (I, [P, P, I, P, I64, I64, I, I, ctypes.c_float, I, P, I64, I64, P, P, SZ, P]),
         "qgemm_tune_lookup": (I, [I, I, I, P, P]),
         "qgemm_tune_record": (I, [I, I, I, I, I]),
         "qgemm_tune_clear": (I, []),
@@ -338,6 +356,168 @@ def qgemm_kv_dequantize(codes, scales, bits, v, stream=None):
                                  _dev(scales, torch.float16, "scales"), nvec, D, int(bits),
                                  _dev(v, torch.float16, "v"), _stream(stream)), "qgemm_kv_dequantize")
     return v
+
+
+# ---------------------------------------------------------- paged KV cache
+
+def qgemm_kv_page_words(kv_heads: int, head_dim: int, k_bits: int, v_bits: int, page_size: int) -> int:
+    """32-bit words of one page of a paged KV cache (see include/qgemm.h)."""
+    return _ok(_lib.qgemm_kv_page_words(kv_heads, head_dim, k_bits, v_bits, page_size), "qgemm_kv_page_words")
+
+
+class KVCache:
+    """A paged KV cache's pages and geometry: the handle that qgemm_kv_append,
+    qgemm_kv_gather and qgemm_kv_attend take.  `pages` is an int32 CUDA tensor
+    whose first dimension counts the pages (qgemm_kv_page_words words each);
+    KVCache.zeros makes one.  Keeps a reference to the tensor, no copy."""
+
+    def __init__(self, pages, page_size, kv_heads, head_dim, k_bits, v_bits):
+        import torch
+        words = qgemm_kv_page_words(kv_heads, head_dim, k_bits, v_bits, page_size)
+        if pages.dim() < 1 or pages.shape[0] < 1 or pages.numel() != pages.shape[0] * words:
+            _shape_error(f"pages must be [num_pages >= 1, ...] with {words} words a page, got {tuple(pages.shape)}")
+        ptr = _dev(pages, (torch.int32, torch.uint32), "pages")
+        self.pages, self.device = pages, pages.device
+        self.page_size, self.kv_heads, self.head_dim = int(page_size), int(kv_heads), int(head_dim)
+        self.k_bits, self.v_bits = int(k_bits), int(v_bits)
+        self._c = _CacheStruct(ptr, pages.shape[0], self.page_size, self.kv_heads, self.head_dim, self.k_bits,
+                               self.v_bits)
+        self._ref = ctypes.byref(self._c)
+
+    @classmethod
+    def zeros(cls, num_pages, page_size, kv_heads, head_dim, k_bits, v_bits, device="cuda"):
+        import torch
+        words = qgemm_kv_page_words(kv_heads, head_dim, k_bits, v_bits, page_size)
+        tiles = page_size // 32
+        pages = torch.zeros(num_pages, kv_heads, tiles, words // (kv_heads * tiles), dtype=torch.int32, device=device)
+        return cls(pages, page_size, kv_heads, head_dim, k_bits, v_bits)
+
+
+class KVBatch:
+    """The sequences of a call: block_table int32 [B, max_pages], seq_lens
+    int32 [B] and cu_new int32 [B + 1] (CUDA tensors; the last cu_new[b + 1] -
+    cu_new[b] tokens of sequence b are the call's rows).  Their values are read
+    when a call runs, so they may be updated in place between calls or replays."""
+
+    def __init__(self, block_table, seq_lens, cu_new):
+        import torch
+        i32 = torch.int32
+        if block_table.dim() != 2 or seq_lens.dim() != 1 or cu_new.dim() != 1:
+            _shape_error("block_table must be [B, max_pages], seq_lens [B], cu_new [B + 1]")
+        B, P = block_table.shape
+        if seq_lens.shape[0] != B or cu_new.shape[0] != B + 1:
+            _shape_error(f"block_table has {B} rows, seq_lens {seq_lens.shape[0]} entries, "
+                         f"cu_new {cu_new.shape[0]} (B + 1 expected)")
+        if block_table.is_cuda and (block_table.dtype is i32) and (P <= 1 or block_table.stride(1) == 1):
+            stride = block_table.stride(0) if B > 1 else P
+            if stride < P:
+                _shape_error("block_table's rows overlap")
+            table = block_table.data_ptr()
+        else:
+            table, stride = _dev(block_table, i32, "block_table"), P  # names what is wrong
+        self.device = block_table.device
+        if seq_lens.device != self.device or cu_new.device != self.device:
+            raise ValueError("block_table, seq_lens and cu_new must be on one device")
+        self._keep = (block_table, seq_lens, cu_new)
+        self._c = _BatchStruct(table, stride, _dev(seq_lens, i32, "seq_lens"), _dev(cu_new, i32, "cu_new"), B, P)
+        self._ref = ctypes.byref(self._c)
+
+
+def _kv_rows(t, name, heads, D, dtype):
+    """Address and strides of a [rows, heads, D] operand."""
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != D:
+        _shape_error(f"{name} must be [rows, {heads}, {D}], got {tuple(t.shape)}")
+    if not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must have dtype {dtype}, got {t.dtype}")
+    rs, hs, es = t.stride()
+    if es != 1:
+        raise ValueError(f"{name}'s last dimension must be contiguous")
+    return t.data_ptr(), rs, hs
+
+
+def _kv_dtype(t, name):
+    import torch
+    if t.dtype is torch.float16:
+        return QGEMM_F16
+    if t.dtype is torch.bfloat16:
+        return QGEMM_BF16
+    raise TypeError(f"{name} must be float16 or bfloat16, got {t.dtype}")
+
+
+def _kv_devices(cache, batch, *tensors):
+    import torch
+    dev = cache.device
+    if dev.index != torch.cuda.current_device():
+        raise ValueError(f"cache on {dev}, but the current device is cuda:{torch.cuda.current_device()}")
+    if batch.device != dev:
+        raise ValueError(f"cache on {dev}, batch on {batch.device}")
+    for t in tensors:
+        if t.device != dev:
+            raise ValueError(f"tensor on {t.device}, cache on {dev}")
+
+
+def _kv_move(fn, name, cache, batch, k, v, stream):
+    dt = _kv_dtype(k, "k")
+    kp, krs, khs = _kv_rows(k, "k", cache.kv_heads, cache.head_dim, k.dtype)
+    vp, vrs, vhs = _kv_rows(v, "v", cache.kv_heads, cache.head_dim, k.dtype)
+    if v.shape[0] != k.shape[0]:
+        _shape_error(f"k has {k.shape[0]} rows, v has {v.shape[0]}")
+    _kv_devices(cache, batch, k, v)
+    _ok(fn(cache._ref, batch._ref, k.shape[0], kp, krs, khs, vp, vrs, vhs, dt, _stream(stream)), name)
+
+
+def qgemm_kv_append(k, v, cache, batch, stream=None):
+    """Quantise the batch's new tokens k, v [rows, kv_heads, D] (fp16 or bf16,
+    any row and head stride) into their pages."""
+    _kv_move(_lib.qgemm_kv_append, "qgemm_kv_append", cache, batch, k, v, stream)
+    return cache
+
+
+def qgemm_kv_gather(cache, batch, k, v, stream=None):
+    """Read the batch's last tokens back into k, v [rows, kv_heads, D]."""
+    _kv_move(_lib.qgemm_kv_gather, "qgemm_kv_gather", cache, batch, k, v, stream)
+    return k, v
+
+
+def qgemm_kv_attend(q, cache, batch, out, ws, scale=None, window=0, lse=None, stream=None):
+    """Causal attention of the batch's new rows q [rows, q_heads, D] over their
+    sequences in the cache -> out (q's shape and dtype) and, if given, lse fp32
+    [rows, q_heads].  scale defaults to D ** -0.5; window > 0 keeps the last
+    `window` positions of each row.  ws: kv_workspace(cache, q_heads)."""
+    import torch
+    dt = _kv_dtype(q, "q")
+    if q.dim() != 3:
+        _shape_error("q must be [rows, q_heads, D]")
+    T, Hq, D = q.shape
+    qp, qrs, qhs = _kv_rows(q, "q", Hq, cache.head_dim, q.dtype)
+    op, ors, ohs = _kv_rows(out, "out", Hq, cache.head_dim, q.dtype)
+    if Hq == 0 or Hq % cache.kv_heads:
+        _shape_error(f"q_heads = {Hq} is not a multiple of kv_heads = {cache.kv_heads}")
+    if out.shape[0] != T:
+        _shape_error(f"q has {T} rows, out has {out.shape[0]}")
+    if lse is None:
+        _kv_devices(cache, batch, q, out, ws)
+        lp = None
+    else:
+        if lse.dim() != 2 or lse.shape[0] != T or lse.shape[1] != Hq:
+            _shape_error(f"lse must be [{T}, {Hq}], got {tuple(lse.shape)}")
+        _kv_devices(cache, batch, q, out, ws, lse)
+        lp = _dev(lse, torch.float32, "lse")
+    _ok(_lib.qgemm_kv_attend(cache._ref, batch._ref, T, qp, qrs, qhs, dt, Hq, D ** -0.5 if scale is None else scale,
+                             window, op, ors, ohs, lp, _dev(ws, torch.uint8, "ws"), ws.numel(), _stream(stream)),
+        "qgemm_kv_attend")
+    return out
+
+
+def kv_workspace(cache, q_heads: int):
+    """A zero-filled workspace of the size qgemm_kv_attend needs."""
+    import torch
+    n = int(_lib.qgemm_kv_attend_workspace_bytes(cache._ref, int(q_heads)))
+    if n == 0:
+        _shape_error(f"q_heads = {q_heads} is not a multiple of kv_heads = {cache.kv_heads}")
+    return torch.zeros(n, dtype=torch.uint8, device=cache.device)
 
 
 def qgemm(x, perm, qw, scales, bits, offs, y, ws=None, stream=None):

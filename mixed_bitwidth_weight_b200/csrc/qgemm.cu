@@ -17,6 +17,7 @@
 #include "gemm.cuh"
 #include "quantize.cuh"
 #include "kv_cache.cuh"
+#include "kv_paged.cuh"
 
 namespace {
 
@@ -858,6 +859,83 @@ void launch_kv_quant(dim3 grid, dim3 block, cudaStream_t s, const __half* v, int
     }
 }
 
+// ------------------------------------------------------- paged KV cache
+bool kv_bits_ok(int b) { return b == 2 || b == 3 || b == 4 || b == 5 || b == 6 || b == 8; }
+
+int check_kv_geometry(int heads, int D, int kb, int vb, int page_size) {
+    if (heads < 1 || heads > 1024 || (D != 64 && D != 128 && D != 256)) return QGEMM_ERR_SHAPE;
+    if (page_size < kTileTokens || page_size > 4096 || (page_size & (page_size - 1))) return QGEMM_ERR_SHAPE;
+    return kv_bits_ok(kb) && kv_bits_ok(vb) ? QGEMM_OK : QGEMM_ERR_BITS;
+}
+
+int64_t kv_page_bytes(int heads, int D, int kb, int vb, int page_size) {
+    return (int64_t)heads * (page_size / kTileTokens) * 4 * D * (kb + vb + 1);
+}
+
+// checks a cache and a batch and turns them into the kernels' structs
+int kv_setup(const qgemm_kv_cache* c, const qgemm_kv_batch* b, int num_rows, KvPages* pg, KvBatch* bt) {
+    if (!c || !b || !c->d_pages) return QGEMM_ERR_NULL;
+    int st = check_kv_geometry(c->kv_heads, c->head_dim, c->k_bits, c->v_bits, c->page_size);
+    if (st != QGEMM_OK) return st;
+    if (c->num_pages < 1 || c->num_pages > 0x7fffffff) return QGEMM_ERR_SHAPE;
+    if (b->num_seqs < 0 || b->num_seqs > 65535 || num_rows < 0 || b->max_pages < 0 ||
+        b->table_stride < b->max_pages)
+        return QGEMM_ERR_SHAPE;
+    if (b->num_seqs > 0 && (!b->d_seq_lens || !b->d_cu_new || (b->max_pages > 0 && !b->d_block_table)))
+        return QGEMM_ERR_NULL;
+    if (((uintptr_t)c->d_pages & 127) || ((uintptr_t)b->d_block_table & 3) || ((uintptr_t)b->d_seq_lens & 3) ||
+        ((uintptr_t)b->d_cu_new & 3))
+        return QGEMM_ERR_ALIGN;
+    *pg = KvPages{reinterpret_cast<uint8_t*>(c->d_pages), c->num_pages,
+                  kv_page_bytes(c->kv_heads, c->head_dim, c->k_bits, c->v_bits, c->page_size),
+                  c->page_size, c->kv_heads, c->k_bits, c->v_bits};
+    *bt = KvBatch{b->d_block_table, b->table_stride, b->d_seq_lens, b->d_cu_new, b->num_seqs, b->max_pages, num_rows};
+    return QGEMM_OK;
+}
+
+// a row operand: alignment, and for written ones no two elements in one place
+int kv_rows(const void* p, int64_t row, int64_t head, int rows, int heads, int D, bool written, KvRows* out) {
+    if (!p) return QGEMM_ERR_NULL;
+    if (!aligned16(p) || (row & 7) || (head & 7)) return QGEMM_ERR_ALIGN;
+    if (row < 0 || head < 0 || row > ((int64_t)1 << 40) || head > ((int64_t)1 << 40)) return QGEMM_ERR_SHAPE;
+    if (written) {
+        const bool by_row = (heads == 1 || head >= D) && (rows == 1 || row >= (heads == 1 ? D : head * (heads - 1) + D));
+        const bool by_head = (rows == 1 || row >= D) && (heads == 1 || head >= (rows == 1 ? D : row * (rows - 1) + D));
+        if (!by_row && !by_head) return QGEMM_ERR_SHAPE;
+    }
+    *out = KvRows{static_cast<uint8_t*>(const_cast<void*>(p)), row, head};
+    return QGEMM_OK;
+}
+
+int kv_move(bool append, const qgemm_kv_cache* cache, const qgemm_kv_batch* batch, int num_rows, const void* d_k, int64_t krs,
+            int64_t khs, const void* d_v, int64_t vrs, int64_t vhs, int dtype, void* stream) {
+    KvPages pg;
+    KvBatch bt;
+    int st = kv_setup(cache, batch, num_rows, &pg, &bt);
+    if (st != QGEMM_OK) return st;
+    if (dtype != QGEMM_F16 && dtype != QGEMM_BF16) return QGEMM_ERR_DTYPE;
+    if (bt.num_seqs == 0 || bt.rows == 0) return QGEMM_OK;
+    KvRows k, v;
+    const int D = cache->head_dim;
+    if ((st = kv_rows(d_k, krs, khs, bt.rows, pg.heads, D, !append, &k)) != QGEMM_OK) return st;
+    if ((st = kv_rows(d_v, vrs, vhs, bt.rows, pg.heads, D, !append, &v)) != QGEMM_OK) return st;
+    const int64_t items = 2 * (int64_t)bt.rows * pg.heads, ctas = (items + kKvWarps - 1) / kKvWarps;
+    if (ctas > 0x7fffffff) return QGEMM_ERR_SHAPE;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const bool bf = dtype == QGEMM_BF16;
+#define QG_KV_MOVE(DD)                                                                         \
+    if (D == DD) {                                                                             \
+        auto f = append ? (bf ? kv_append_kernel<DD, true> : kv_append_kernel<DD, false>)      \
+                        : (bf ? kv_gather_kernel<DD, true> : kv_gather_kernel<DD, false>);     \
+        f<<<(unsigned)ctas, 32 * kKvWarps, 0, s>>>(pg, bt, k, v);                              \
+    }
+    QG_KV_MOVE(64)
+    QG_KV_MOVE(128)
+    QG_KV_MOVE(256)
+#undef QG_KV_MOVE
+    return launch_status();
+}
+
 }  // namespace
 
 // =========================================================== C ABI
@@ -1200,6 +1278,63 @@ int qgemm_kv_dequantize(const uint32_t* d_codes, const uint16_t* d_scales, int64
         case 4: kv_dequant_kernel<4><<<grid, block, 0, s>>>(d_codes, sc, nvec, bits, v); break;
         default: kv_dequant_kernel<8><<<grid, block, 0, s>>>(d_codes, sc, nvec, bits, v); break;
     }
+    return launch_status();
+}
+
+int64_t qgemm_kv_page_words(int kv_heads, int head_dim, int k_bits, int v_bits, int page_size) {
+    const int st = check_kv_geometry(kv_heads, head_dim, k_bits, v_bits, page_size);
+    return st != QGEMM_OK ? st : kv_page_bytes(kv_heads, head_dim, k_bits, v_bits, page_size) / 4;
+}
+
+int qgemm_kv_append(const qgemm_kv_cache* cache, const qgemm_kv_batch* batch, int num_rows, const void* d_k, int64_t k_row_stride,
+                    int64_t k_head_stride, const void* d_v, int64_t v_row_stride, int64_t v_head_stride, int dtype,
+                    void* stream) {
+    return kv_move(true, cache, batch, num_rows, d_k, k_row_stride, k_head_stride, d_v, v_row_stride, v_head_stride, dtype,
+                   stream);
+}
+
+int qgemm_kv_gather(const qgemm_kv_cache* cache, const qgemm_kv_batch* batch, int num_rows, void* d_k, int64_t k_row_stride,
+                    int64_t k_head_stride, void* d_v, int64_t v_row_stride, int64_t v_head_stride, int dtype,
+                    void* stream) {
+    return kv_move(false, cache, batch, num_rows, d_k, k_row_stride, k_head_stride, d_v, v_row_stride, v_head_stride, dtype,
+                   stream);
+}
+
+size_t qgemm_kv_attend_workspace_bytes(const qgemm_kv_cache* c, int q_heads) {
+    if (!c || check_kv_geometry(c->kv_heads, c->head_dim, c->k_bits, c->v_bits, c->page_size) != QGEMM_OK ||
+        q_heads < 1 || q_heads % c->kv_heads)
+        return 0;
+    return 16;
+}
+
+int qgemm_kv_attend(const qgemm_kv_cache* cache, const qgemm_kv_batch* batch, int num_rows, const void* d_q, int64_t q_row_stride,
+                    int64_t q_head_stride, int dtype, int q_heads, float scale, int window, void* d_out,
+                    int64_t out_row_stride, int64_t out_head_stride, float* d_lse, void* d_ws, size_t ws_bytes,
+                    void* stream) {
+    KvAttend a;
+    int st = kv_setup(cache, batch, num_rows, &a.pg, &a.bt);
+    if (st != QGEMM_OK) return st;
+    if (dtype != QGEMM_F16 && dtype != QGEMM_BF16) return QGEMM_ERR_DTYPE;
+    if (q_heads < 1 || q_heads > 65536 || q_heads % a.pg.heads || window < 0 || !std::isfinite(scale))
+        return QGEMM_ERR_SHAPE;
+    if (!d_ws || ws_bytes < qgemm_kv_attend_workspace_bytes(cache, q_heads)) return QGEMM_ERR_WORKSPACE;
+    if (!aligned16(d_ws) || ((uintptr_t)d_lse & 3)) return QGEMM_ERR_ALIGN;
+    if (a.bt.num_seqs == 0 || a.bt.rows == 0) return QGEMM_OK;
+    const int D = cache->head_dim;
+    if ((st = kv_rows(d_q, q_row_stride, q_head_stride, a.bt.rows, q_heads, D, false, &a.q)) != QGEMM_OK) return st;
+    if ((st = kv_rows(d_out, out_row_stride, out_head_stride, a.bt.rows, q_heads, D, true, &a.out)) != QGEMM_OK)
+        return st;
+    a.lse = d_lse;
+    a.q_heads = q_heads;
+    a.window = window;
+    a.scale = scale;
+    const dim3 grid(a.pg.heads, a.bt.num_seqs);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const bool bf = dtype == QGEMM_BF16;
+    auto f = D == 64 ? (bf ? kv_attend_kernel<64, true> : kv_attend_kernel<64, false>)
+             : D == 128 ? (bf ? kv_attend_kernel<128, true> : kv_attend_kernel<128, false>)
+                        : (bf ? kv_attend_kernel<256, true> : kv_attend_kernel<256, false>);
+    f<<<grid, 32 * kKvWarps, 0, s>>>(a);
     return launch_status();
 }
 
