@@ -1,0 +1,1005 @@
+// Attention of new tokens over the paged, quantised KV cache (layout in
+// kv_paged.cuh), without expanding it.
+//
+//   out_n = sum_t p_tn v'_t / sum_t p_tn,  p_tn = exp(scale q_n . k'_t),
+//   k' = H u_k / D, v' = H u_v / D, u = (c - z) s_g, z = 2^(b-1), H H = D I.
+// H is symmetric, so q . k' = (H q) . u_k / D and sum_t p v' = H (sum_t p u_v) / D:
+// each query row is rotated once, each output row once, and the cache's codes
+// meet the matrix instructions as they are.
+//
+// Scores, per group g of 32 dims: sum_d (Hq)_d (c - z) on m16n8k16 with the
+// codes as the A operand (16 tokens), 8 query rows as B.  A code's bits, masked
+// out of its word, ARE an fp16 number: the subnormal c 2^-24 (in place, i bits
+// further up, c 2^(i-24); the query carries 2^-i).  So a pair of codes costs one
+// AND.  The accumulators start at -z sum_d (Hq)_d instead of 0, and the token's
+// scale multiplies the group's sum in fp32.  The rotated query is held as two
+// fp16 parts (22 bits), each times the exact codes.
+// Output: A = codes of V (16 dims x 16 tokens; c - z by one exact subtraction
+// per pair: starting at -z sum p would lose the sum of many tokens to
+// cancellation), B = p s_g, rounded to fp16 after p and s are (two roundings of
+// 2^-12 on average per weight; the sum of weights is not rounded).  p is kept
+// near 2^10 and s below 2 (2^-E of the largest seen) so that weights keep 11
+// bits down to 2^-24 of the largest.  P turns from the accumulators' layout to
+// the B operand's by movmatrix.
+//
+// The legacy matrix instruction, because its operands are registers: a code is
+// masked into place and multiplied without a store.  tcgen05 would need every
+// expanded tile written to tensor or shared memory first (the V tile transposed),
+// and 8 query rows fill 1/16 of its M.  m16n8k16 runs at 2.1 cycles per SM here;
+// 24 of them per 16 tokens of 128 dims are 50 cycles against the 100 the codes
+// (144 bytes a token at 4 bits) take from HBM.
+//
+// Work: the (sequence, head, block of rows, 32-token tile) space is cut into equal
+// runs per CTA and per warp, whatever the lengths (both read on the device).  A
+// warp walks its run with a ring of bulk copies (one record each); what it has of
+// an item is joined in shared memory per CTA, and across CTAs by the last one
+// to arrive, in a fixed order.
+#pragma once
+
+#include "kv_paged.cuh"
+
+namespace qg {
+
+struct KvAttend {
+    KvPages pg;
+    KvBatch bt;
+    KvRows q, out;
+    float* lse;  // [rows][q_heads] or null
+    int32_t q_heads, group, window, stages;
+    float scale;
+    unsigned int* tickets;  // [CTAs], zero between calls
+    float* partial;         // [CTAs][2] slots
+};
+
+constexpr int kAttMaxStages = 8;
+constexpr float kAttShift = 10.f;    // weights are 2^(x - m + 10)
+constexpr float kAttSlack = 4.f;     // the running maximum may be this far behind (log2)
+
+template <int D, int NT>
+struct AttCfg {
+    static constexpr int W = D * NT <= 128 ? 16 : 8;  // warps
+    static constexpr int G = D / 32;
+    static constexpr int RB = 8 * NT;                 // query rows of an item
+    static constexpr int OS = D + 4;                  // row stride of a slot: conflict-free float4 stores
+    static constexpr int SlotFloats = RB * OS + 2 * RB;
+    static constexpr int SlotBytes = SlotFloats * 4;
+    static constexpr int GSlot = RB * D + 2 * RB;     // floats of a global slot
+    // shared memory: slots, stage descriptors, barriers, fragments, rings
+    static constexpr int DescAt = W * SlotBytes;
+    static constexpr int BarAt = DescAt + W * 8 * 16;
+    static constexpr int FragAt = BarAt + W * 8 * 8;
+    static constexpr int RingAt = (FragAt + 2 * W * 24 + 127) / 128 * 128;
+};
+
+// a slot's fragment: tiles [a, b) of the item whose first tile is number `item`
+struct AttFrag {
+    long long item;
+    int seq, head, rb, tiles;  // the item; tiles = all its tiles, 0 = no fragment
+};
+static_assert(sizeof(AttFrag) == 24 && kAttMaxStages == 8, "the shared-memory layout");
+
+QG_DEV void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+QG_DEV uint32_t movm_trans(uint32_t a) {
+    uint32_t d;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+    return d;
+}
+
+QG_DEV float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+QG_DEV uint32_t h2_bits(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
+QG_DEV __half2 bits_h2(uint32_t u) { return *reinterpret_cast<__half2*>(&u); }
+
+// ------------------------------------------------------------ code extraction
+// Fields of one 32-bit word: its low half holds n codes of one row, its high
+// half the n codes that pair with them (n = 4 for b <= 4, else 2).  Field i is
+// used where it lies when it ends below bit 10 (a subnormal's mantissa), else
+// the word is shifted down first.
+template <int B>
+struct Fld {
+    static constexpr int N = B <= 4 ? 4 : 2;
+    static constexpr int pre(int i) { return B * i + B <= 10 ? 0 : (B == 4 ? 8 : B * i); }
+    static constexpr int at(int i) { return B * i - pre(i); }  // the value is c 2^(at - 24)
+    static constexpr uint32_t mask(int i) { return (((1u << B) - 1u) << at(i)) * 0x10001u; }
+    static constexpr uint32_t zero(int i) { return ((1u << (B - 1)) << at(i)) * 0x10001u; }
+};
+
+template <int B, int I>
+QG_DEV uint32_t field(uint32_t x) {
+    if constexpr (Fld<B>::pre(I) == 0) return x & Fld<B>::mask(I);
+    return (x >> Fld<B>::pre(I)) & Fld<B>::mask(I);
+}
+
+// shift a run-time width's field i carries (for the query and the output)
+QG_DEV int field_at(int b, int i) {
+    i = b <= 4 ? i : (i & 1);
+    if (b * i + b <= 10) return b * i;
+    return b == 4 ? b * i - 8 : 0;
+}
+
+// a register whose low bits are the stream's from bit `pos` on (pos constant after unrolling)
+template <int NW>
+QG_DEV uint32_t bits_from(const uint32_t (&w)[NW], int pos, int need) {
+    const int i = pos >> 5, o = pos & 31;
+    if (o == 0) return w[i];
+    if (o + need <= 32) return w[i] >> o;
+    return __funnelshift_r(w[i], w[i + 1], o);
+}
+
+// (low half: bits from p0; high half: bits from p1); the fields' masks drop the rest
+template <int NW>
+QG_DEV uint32_t halves_from(const uint32_t (&w)[NW], int p0, int p1, int need) {
+    uint32_t a, b;
+    int ya, yb;
+    if ((p0 & 7) == 0 && (p0 & 31) + 16 <= 32) {
+        a = w[p0 >> 5];
+        ya = (p0 & 31) >> 3;
+    } else {
+        a = bits_from(w, p0, need);
+        ya = 0;
+    }
+    if ((p1 & 7) == 0 && (p1 & 31) + 16 <= 32) {
+        b = w[p1 >> 5];
+        yb = (p1 & 31) >> 3;
+    } else {
+        b = bits_from(w, p1, need);
+        yb = 0;
+    }
+    return __byte_perm(a, b, ya | (ya + 1) << 4 | (yb + 4) << 8 | (yb + 5) << 12);
+}
+
+// K: the low and high four (b <= 4) or two codes of a unit part, side by side
+template <int B, int NW>
+QG_DEV uint32_t k_word(const uint32_t (&w)[NW], int pos) {
+    if constexpr (B == 4 || B == 8) {
+        return w[pos >> 5];
+    } else if constexpr (B == 2) {
+        const int y = (pos & 31) >> 3;
+        return __byte_perm(w[pos >> 5], 0, y | y << 4 | (y + 1) << 8 | (y + 1) << 12);
+    } else {
+        constexpr int gap = B == 3 ? 12 : 2 * B;
+        const uint32_t t = bits_from(w, pos, 2 * gap);
+        return (t & 0xffffu) | ((t << (16 - gap)) & 0xffff0000u);
+    }
+}
+
+// half a tile's words of this lane's stream
+template <int D, int B>
+QG_DEV void load_words(const uint8_t* part, int half, int lane, uint32_t (&w)[D * B / 64]) {
+    constexpr int NW = D * B / 64;
+    constexpr int V = NW % 4 == 0 ? 4 : NW % 2 == 0 ? 2 : 1;
+#pragma unroll
+    for (int c = 0; c < NW / V; ++c) {
+        const uint8_t* p = part + ((half * (NW / V) + c) * 32 + lane) * (4 * V);
+        if constexpr (V == 4) {
+            const uint4 u = *reinterpret_cast<const uint4*>(p);
+            w[4 * c] = u.x;
+            w[4 * c + 1] = u.y;
+            w[4 * c + 2] = u.z;
+            w[4 * c + 3] = u.w;
+        } else if constexpr (V == 2) {
+            const uint2 u = *reinterpret_cast<const uint2*>(p);
+            w[2 * c] = u.x;
+            w[2 * c + 1] = u.y;
+        } else {
+            w[c] = *reinterpret_cast<const uint32_t*>(p);
+        }
+    }
+}
+
+// ------------------------------------------------------------------- scores
+// The query rows of an item in the B operand's layout: hi and lo parts, per
+// group and k step two registers, and -z 2^-24 times their sums.
+template <int D, int NT>
+struct AttQ {
+    uint32_t hi[NT][D / 32][4], lo[NT][D / 32][4];
+    float zq[NT][D / 32][2];
+    float f[NT][2];  // factor of a score, log2 units
+};
+
+template <int D, int NT, int B>
+QG_DEV void scores_half(const uint8_t* rec, int half, int lane, const AttQ<D, NT>& q, float (&s)[NT][4]) {
+    constexpr int G = D / 32, NW = D * B / 64;
+    uint32_t w[NW];
+    load_words<D, B>(rec, half, lane, w);
+    // scales of tokens 16 half + r and + 8, groups in pairs
+    uint32_t sc[G];
+    {
+        const uint8_t* p = rec + 4 * D * B + (((lane >> 2) * 4 + 2 * half) * G) * 2;
+        if constexpr (G == 2) {
+            const uint2 u = *reinterpret_cast<const uint2*>(p);
+            sc[0] = u.x;
+            sc[1] = u.y;
+        } else {
+#pragma unroll
+            for (int i = 0; i < G; i += 4) {
+                const uint4 u = *reinterpret_cast<const uint4*>(p + 4 * i);
+                sc[i] = u.x;
+                sc[i + 1] = u.y;
+                sc[i + 2] = u.z;
+                sc[i + 3] = u.w;
+            }
+        }
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[nt][i] = 0.f;
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+        const int p0 = g * 8 * B, p1 = (G + g) * 8 * B;  // units of the two tokens
+        uint32_t a[8];
+        if constexpr (B <= 4) {
+            const uint32_t x0 = k_word<B>(w, p0), x1 = k_word<B>(w, p1);
+            a[0] = field<B, 0>(x0);
+            a[1] = field<B, 0>(x1);
+            a[2] = field<B, 1>(x0);
+            a[3] = field<B, 1>(x1);
+            a[4] = field<B, 2 % Fld<B>::N>(x0);
+            a[5] = field<B, 2 % Fld<B>::N>(x1);
+            a[6] = field<B, 3 % Fld<B>::N>(x0);
+            a[7] = field<B, 3 % Fld<B>::N>(x1);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const uint32_t x0 = k_word<B>(w, p0 + 4 * B * k), x1 = k_word<B>(w, p1 + 4 * B * k);
+                a[4 * k] = field<B, 0>(x0);
+                a[4 * k + 1] = field<B, 0>(x1);
+                a[4 * k + 2] = field<B, 1>(x0);
+                a[4 * k + 3] = field<B, 1>(x1);
+            }
+        }
+        const __half2 h0 = bits_h2(sc[g / 2]), h1 = bits_h2(sc[G / 2 + g / 2]);
+        const float s0 = (g & 1) ? __high2float(h0) : __low2float(h0);
+        const float s1 = (g & 1) ? __high2float(h1) : __low2float(h1);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            float c[4] = {q.zq[nt][g][0], q.zq[nt][g][1], q.zq[nt][g][0], q.zq[nt][g][1]};
+            mma_f16(c, a[0], a[1], a[2], a[3], q.hi[nt][g][0], q.hi[nt][g][1]);
+            mma_f16(c, a[4], a[5], a[6], a[7], q.hi[nt][g][2], q.hi[nt][g][3]);
+            mma_f16(c, a[0], a[1], a[2], a[3], q.lo[nt][g][0], q.lo[nt][g][1]);
+            mma_f16(c, a[4], a[5], a[6], a[7], q.lo[nt][g][2], q.lo[nt][g][3]);
+            s[nt][0] = fmaf(c[0], s0, s[nt][0]);
+            s[nt][1] = fmaf(c[1], s0, s[nt][1]);
+            s[nt][2] = fmaf(c[2], s1, s[nt][2]);
+            s[nt][3] = fmaf(c[3], s1, s[nt][3]);
+        }
+    }
+}
+
+// Rotate this warp's query rows (lane 4 n + j: row n's dims 32 g + 8 j + i) and
+// split them.  Butterflies in fp32: strides 1, 2, 4 within the lane, 8 and 16
+// between the four lanes of a row, the rest within the lane.
+template <int D, int NT, bool BF16>
+QG_DEV void load_queries(const KvAttend& a, int row0, int rows, int r_base, int head, int lane, AttQ<D, NT>& q) {
+    constexpr int G = D / 32;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        const int j = lane & 3, r = r_base + nt * 8 + (lane >> 2);
+        float x[G][8];
+        if (r < rows) {
+            const int tok = r / a.group, hq = head * a.group + (r - tok * a.group);
+            const uint16_t* p = reinterpret_cast<const uint16_t*>(a.q.p) + (row0 + tok) * a.q.row + hq * a.q.head;
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+                const uint4 u = __ldg(reinterpret_cast<const uint4*>(p + 32 * g + 8 * j));
+                const uint32_t v[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    x[g][i] = kv_to_float<BF16>((uint16_t)((i & 1) ? v[i / 2] >> 16 : v[i / 2] & 0xffff));
+            }
+        } else {
+#pragma unroll
+            for (int g = 0; g < G; ++g)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[g][i] = 0.f;
+        }
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+#pragma unroll
+            for (int st = 1; st < 8; st <<= 1)
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (!(i & st)) {
+                        const float u = x[g][i], v = x[g][i + st];
+                        x[g][i] = u + v;
+                        x[g][i + st] = u - v;
+                    }
+#pragma unroll
+            for (int ls = 1; ls < 4; ls <<= 1)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float o = __shfl_xor_sync(0xffffffffu, x[g][i], ls);
+                    x[g][i] = (lane & ls) ? o - x[g][i] : x[g][i] + o;
+                }
+        }
+#pragma unroll
+        for (int st = 1; st < G; st <<= 1)
+#pragma unroll
+            for (int g = 0; g < G; ++g)
+                if (!(g & st))
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float u = x[g][i], v = x[g + st][i];
+                        x[g][i] = u + v;
+                        x[g + st][i] = u - v;
+                    }
+        // largest magnitude into [2^14, 2^15): both fp16 parts keep their bits
+        float amax = 0.f;
+#pragma unroll
+        for (int g = 0; g < G; ++g)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(x[g][i]));
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+        int e = (int)(__float_as_uint(amax) >> 23) - 127;  // 128 for infinity: no scaling then
+        e = e >= 128 ? 14 : max(e, -100);
+        const float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
+        const float f = a.scale * (1.4426950408889634f / (float)D) * 16777216.f *
+                        __uint_as_float((uint32_t)(127 - 14 + e) << 23);
+        float dn[4];  // what pair i's place in its word multiplies a code by
+#pragma unroll
+        for (int i = 0; i < 4; ++i) dn[i] = __uint_as_float((uint32_t)(127 - field_at(a.pg.kb, i)) << 23);
+        const float z = (float)(1 << (a.pg.kb - 1)) * 5.9604644775390625e-8f;
+        const int src = (lane & 3) * 8;  // lane of row 2j (4 * 2j)
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+            float sum = 0.f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float u = x[g][i] * up, v = x[g][i + 4] * up, ud = u * dn[i], vd = v * dn[i];
+                const __half2 hi = __floats2half2_rn(ud, vd);
+                const __half2 lo = __floats2half2_rn(ud - __low2float(hi), vd - __high2float(hi));
+                q.hi[nt][g][i] = h2_bits(hi);
+                q.lo[nt][g][i] = h2_bits(lo);
+                sum += u + v;
+            }
+            sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+            sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+            q.zq[nt][g][0] = -z * __shfl_sync(0xffffffffu, sum, src);
+            q.zq[nt][g][1] = -z * __shfl_sync(0xffffffffu, sum, src + 4);
+        }
+        q.f[nt][0] = __shfl_sync(0xffffffffu, f, src);
+        q.f[nt][1] = __shfl_sync(0xffffffffu, f, src + 4);
+    }
+}
+
+// ------------------------------------------------------------------- output
+// acc += (codes of V) x (weights): half a tile.  p[nt][k]: weights of tokens
+// 16 half + 8 k + 2 j + {0, 1} for row n = lane / 4; on[nt][k] their masks.
+template <int D, int NT, int B>
+QG_DEV void output_half(const uint8_t* part, int half, int lane, __half2 es, const uint32_t (&p)[NT][2],
+                        const uint32_t (&on)[NT][2], float (&acc)[NT][D / 16][4]) {
+    constexpr int G = D / 32, NW = D * B / 64, UT = D / 64 * 8 * B;  // bits of a token's units
+    uint32_t w[NW];
+    load_words<D, B>(part, half, lane, w);
+    const uint8_t* scales = part + 4 * D * B + ((lane & 3) * G * 8 + 4 * half) * 2;
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+        const uint2 su = *reinterpret_cast<const uint2*>(scales + g * 16);
+        const __half2 s0 = __hmul2(bits_h2(su.x), es), s1 = __hmul2(bits_h2(su.y), es);
+        uint32_t b0[NT], b1[NT];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            b0[nt] = h2_bits(__hmul2(bits_h2(p[nt][0]), s0)) & on[nt][0];
+            b1[nt] = h2_bits(__hmul2(bits_h2(p[nt][1]), s1)) & on[nt][1];
+        }
+        const int unit = (g >> 1) * 8 * B + (g & 1) * 4 * B;  // this group's four codes in a token's units
+        uint32_t f[2][4];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int t0 = (2 * k) * UT + unit, t1 = (2 * k + 1) * UT + unit;
+            if constexpr (B <= 4) {
+                const uint32_t x = halves_from(w, t0, t1, 4 * B);
+                f[k][0] = field<B, 0>(x);
+                f[k][1] = field<B, 1>(x);
+                f[k][2] = field<B, 2 % Fld<B>::N>(x);
+                f[k][3] = field<B, 3 % Fld<B>::N>(x);
+            } else {
+                const uint32_t x = halves_from(w, t0, t1, 2 * B), y = halves_from(w, t0 + 2 * B, t1 + 2 * B, 2 * B);
+                f[k][0] = field<B, 0>(x);
+                f[k][1] = field<B, 1>(x);
+                f[k][2] = field<B, 0>(y);
+                f[k][3] = field<B, 1>(y);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                f[k][i] = h2_bits(__hsub2(bits_h2(f[k][i]), bits_h2(Fld<B>::zero(i % Fld<B>::N))));
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            mma_f16(acc[nt][2 * g], f[0][0], f[0][1], f[1][0], f[1][1], b0[nt], b1[nt]);
+            mma_f16(acc[nt][2 * g + 1], f[0][2], f[0][3], f[1][2], f[1][3], b0[nt], b1[nt]);
+        }
+    }
+}
+
+// largest V scale among this lane's tokens of the tile, up to slot `last`
+// (slots behind the last visible token may hold anything)
+template <int D>
+QG_DEV __half2 v_scale_max(const uint8_t* part, int vb, int lane, int last) {
+    constexpr int G = D / 32;
+    const uint8_t* scales = part + 4 * D * vb + (lane & 3) * G * 16;
+    __half2 m = bits_h2(0);
+    uint32_t keep[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
+    if (last < kTileTokens - 1) {
+#pragma unroll
+        for (int tt = 0; tt < 4; ++tt) {
+            const int t = 8 * tt + 2 * (lane & 3);
+            keep[tt] = t + 1 <= last ? 0xffffffffu : t <= last ? 0xffffu : 0u;
+        }
+    }
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+        uint4 u = *reinterpret_cast<const uint4*>(scales + g * 16);
+        if (last < kTileTokens - 1) {
+            u.x &= keep[0];
+            u.y &= keep[1];
+            u.z &= keep[2];
+            u.w &= keep[3];
+        }
+        m = __hmax2(m, __hmax2(__hmax2(bits_h2(u.x), bits_h2(u.y)), __hmax2(bits_h2(u.z), bits_h2(u.w))));
+    }
+    return m;
+}
+
+// ------------------------------------------------------------------- the run
+// What a sequence gives: n query rows (x group) in nrb blocks over `tiles` tiles
+// from tile t0 on.  An item has one tile at least, so that empty rows are written.
+struct AttSeq {
+    int row0, n, len, pos0, t0, tiles, nrb;  // pos0: the first row's position
+};
+
+template <int RB>
+QG_DEV AttSeq att_seq(const KvAttend& a, int b) {
+    AttSeq s;
+    s.row0 = max(a.bt.cu[b], 0);
+    const int end = a.bt.cu[b + 1];
+    s.n = min(end, a.bt.rows) - s.row0;
+    s.len = a.bt.lens[b];
+    s.pos0 = s.len - end + s.row0;
+    s.t0 = 0;
+    s.tiles = 1;
+    s.nrb = 0;
+    if (s.n <= 0) return s;
+    s.nrb = (int)(((int64_t)s.n * a.group + RB - 1) / RB);
+    if (s.len <= 0) return s;
+    const int64_t first = a.window > 0 ? (int64_t)s.pos0 - a.window + 1 : 0;
+    s.t0 = (int)(first > 0 ? first / kTileTokens : 0);
+    s.tiles = (int)(((int64_t)s.len + kTileTokens - 1) / kTileTokens) - s.t0;
+    return s;
+}
+
+struct AttCursor {
+    int b, h, rb, tile;
+    AttSeq s;
+};
+
+// where tile number `at` of the call lies; prefix: tiles before each thread's chunk of sequences
+template <int RB>
+QG_DEV void att_seek(const KvAttend& a, const long long* prefix, int nthreads, int chunk, long long at, int lane,
+                     AttCursor& c) {
+    int lo = 0, n = nthreads;
+    while (n > 1) {
+        const int step = (n + 31) / 32, i = lane * step;
+        const bool le = i < n && prefix[lo + i] <= at;
+        const int k = 31 - __clz(__ballot_sync(0xffffffffu, le));
+        lo += k * step;
+        n = min(step, n - k * step);
+    }
+    long long rem = at - prefix[lo];
+    c.b = lo * chunk;
+    for (;; ++c.b) {
+        c.s = att_seq<RB>(a, c.b);
+        const long long work = (long long)c.s.nrb * a.pg.heads * c.s.tiles;
+        if (rem < work || c.b + 1 >= a.bt.num_seqs) break;
+        rem -= work;
+    }
+    const long long item = rem / c.s.tiles;
+    c.tile = (int)(rem - item * c.s.tiles);
+    c.h = (int)(item / c.s.nrb);
+    c.rb = (int)(item - (long long)c.h * c.s.nrb);
+}
+
+// the next tile; `more`: there is one
+template <int RB>
+QG_DEV void att_next(const KvAttend& a, AttCursor& c, bool more) {
+    if (++c.tile < c.s.tiles) return;
+    c.tile = 0;
+    if (++c.rb < c.s.nrb) return;
+    c.rb = 0;
+    if (++c.h < a.pg.heads) return;
+    c.h = 0;
+    if (!more || c.b + 1 >= a.bt.num_seqs) return;
+    do {
+        ++c.b;
+        c.s = att_seq<RB>(a, c.b);
+    } while (c.s.nrb == 0 && c.b + 1 < a.bt.num_seqs);
+}
+
+constexpr int kDescFirst = 1, kDescLast = 2, kDescSkip = 4, kDescHead = 8, kDescTail = 16;
+// First / Last: of the item within this warp's run; Head / Tail: of the item itself
+
+// rotate back, divide and store one row held by a warp (E consecutive dims a lane)
+template <int D, bool BF16>
+QG_DEV void store_row(const KvAttend& a, float (&o)[D / 32], float m, float l, int row0, int r, int head, int lane) {
+    constexpr int E = D / 32;
+    fwht_warp<E>(o, lane);
+    const int tok = r / a.group, hq = head * a.group + (r - tok * a.group);
+    const float inv = l == 0.f ? 0.f : 1.f / (l * (float)D);
+    uint16_t v[E];
+#pragma unroll
+    for (int i = 0; i < E; ++i) v[i] = kv_from_float<BF16>(o[i] * inv);
+    uint16_t* p = reinterpret_cast<uint16_t*>(a.out.p) + (row0 + tok) * a.out.row + hq * a.out.head + E * lane;
+    if constexpr (E == 2) {
+        *reinterpret_cast<uint32_t*>(p) = v[0] | (uint32_t)v[1] << 16;
+    } else {
+#pragma unroll
+        for (int i = 0; i < E; i += 4)
+            *reinterpret_cast<uint2*>(p + i) = make_uint2(v[i] | (uint32_t)v[i + 1] << 16, v[i + 2] | (uint32_t)v[i + 3] << 16);
+    }
+    if (a.lse && lane == 0)
+        a.lse[(int64_t)(row0 + tok) * a.q_heads + hq] = (m + log2f(l) - kAttShift) * 0.6931471805599453f;
+}
+
+template <int D, int NT, bool BF16>
+__global__ void __launch_bounds__(32 * AttCfg<D, NT>::W, 1) kv_attend_kernel(KvAttend a) {
+    using C = AttCfg<D, NT>;
+    constexpr int W = C::W, G = C::G, RB = C::RB, E = D / 32, T = 32 * W;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    __shared__ long long sh_total[33];
+    __shared__ int sh_last;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int rec_bytes = kv_record_bytes<D>(a.pg.kb, a.pg.vb);
+    float* slots = reinterpret_cast<float*>(smem);
+    int4* descs = reinterpret_cast<int4*>(smem + C::DescAt) + warp * kAttMaxStages;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::BarAt) + warp * kAttMaxStages;
+    AttFrag* frags = reinterpret_cast<AttFrag*>(smem + C::FragAt);
+    uint8_t* rings = smem + C::RingAt;
+    uint8_t* ring = rings + (size_t)warp * a.stages * rec_bytes;
+    long long* prefix = reinterpret_cast<long long*>(smem);  // before the slots are used
+
+    // ---- the call's work, and this CTA's and warp's share
+    const int chunk = (a.bt.num_seqs + T - 1) / T;
+    long long mine = 0;
+    for (int b = threadIdx.x * chunk; b < min((int)(threadIdx.x + 1) * chunk, a.bt.num_seqs); ++b) {
+        const AttSeq s = att_seq<RB>(a, b);
+        mine += (long long)s.nrb * a.pg.heads * s.tiles;
+    }
+    long long inc = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long v = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += v;
+    }
+    if (lane == 31) sh_total[warp] = inc;
+    if (lane < kAttMaxStages) mbar_init(&bars[lane], 1);
+    if (lane < 2) frags[warp * 2 + lane].tiles = 0;
+    fence_mbar_init();
+    __syncthreads();
+    long long before = 0, total = 0;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+        if (w < warp) before += sh_total[w];
+        total += sh_total[w];
+    }
+    prefix[threadIdx.x] = before + inc - mine;
+    __syncthreads();
+    const long long share = max((total + gridDim.x - 1) / gridDim.x, (long long)W);
+    const long long cta0 = min(share * blockIdx.x, total), cta1 = min(cta0 + share, total);
+    if (cta0 >= cta1) return;
+    const long long per = (cta1 - cta0 + W - 1) / W;
+    const long long w0 = min(cta0 + per * warp, cta1), w1 = min(w0 + per, cta1);
+    AttCursor pc;  // the producer's place
+    long long left = w1 - w0;
+    if (left > 0) att_seek<RB>(a, prefix, T, chunk, w0, lane, pc);
+    __syncthreads();  // prefix is read; slots may be written
+
+    // ---- one warp's run
+    const int lps = 31 - __clz(a.pg.page_size / kTileTokens);  // log2 tiles per page
+    int page_base = -1, page_b = -1, page_id = 0;              // lane i: page page_base + i of sequence page_b
+    bool first_of_run = true;
+    bool dead = false;
+    auto issue = [&](int s) {
+        const int T0 = pc.s.t0 + pc.tile;
+        int flags = (first_of_run || pc.tile == 0 ? kDescFirst : 0) | (left == 1 || pc.tile + 1 == pc.s.tiles ? kDescLast : 0) |
+                    (pc.tile == 0 ? kDescHead : 0) | (pc.tile + 1 == pc.s.tiles ? kDescTail : 0);
+        first_of_run = false;
+        const int pi = T0 >> lps;
+        if (page_b != pc.b || pi < page_base || pi >= page_base + 32) {
+            page_b = pc.b;
+            page_base = pi;
+            page_id = pi + lane < a.bt.max_pages && (int64_t)(pi + lane) * a.pg.page_size < pc.s.len
+                          ? a.bt.table[pc.b * a.bt.table_stride + pi + lane]
+                          : -1;
+        }
+        const int page = __shfl_sync(0xffffffffu, page_id, pi - page_base);
+        const bool has = pc.s.len > 0 && page >= 0 && page < a.pg.num_pages && !dead;
+        if (!has) flags |= kDescSkip;
+        if (lane == 0) {
+            if (pc.s.len > 0 && !has && !dead) set_dev_error(QGEMM_DEV_BAD_PAGE);
+            descs[s] = make_int4(pc.b, pc.h | flags << 16, pc.rb, pc.tile);
+            if (has) {
+                const uint8_t* src = a.pg.base + page * a.pg.page_bytes +
+                                     (int64_t)((pc.h << lps) + (T0 & ((1 << lps) - 1))) * rec_bytes;
+                mbar_arrive_expect_tx(&bars[s], rec_bytes);
+                bulk_g2s(ring + (size_t)s * rec_bytes, src, rec_bytes, &bars[s]);
+            } else {
+                mbar_arrive(&bars[s]);
+            }
+        }
+        --left;
+        att_next<RB>(a, pc, left > 0);
+    };
+    int issued = 0;
+    long long done = 0;
+    for (; issued < a.stages && left > 0; ++issued) issue(issued);
+    __syncwarp();
+
+    AttQ<D, NT> q;
+    float acc[NT][2 * G][4], m[NT][2], l[NT][2];
+    AttSeq cs{};
+    int qpos[NT][2], lo_pos = 0, hi_pos = 0, E2 = -14;
+    bool frag_head = false;
+    int stage = 0, parity = 0, in_flight = issued;
+    const int j = lane & 3, r8 = lane >> 2;
+    while (in_flight > 0) {
+        const int4 d = descs[stage];
+        const int flags = d.y >> 16, head = d.y & 0xffff;
+        if (flags & kDescFirst) {
+            cs = att_seq<RB>(a, d.x);
+            const int rows = cs.n * a.group, r_base = d.z * RB;
+            load_queries<D, NT, BF16>(a, cs.row0, rows, r_base, head, lane, q);
+            lo_pos = cs.pos0 + r_base / a.group;
+            hi_pos = cs.pos0 + (min(r_base + RB, rows) - 1) / a.group;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    qpos[nt][c] = cs.pos0 + (r_base + 8 * nt + 2 * j + c) / a.group;
+                    m[nt][c] = -INFINITY;
+                    l[nt][c] = 0.f;
+                }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int i = 0; i < 2 * G; ++i)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) acc[nt][i][c] = 0.f;
+            E2 = -14;
+            frag_head = flags & kDescHead;
+        }
+        if (!mbar_wait(&bars[stage], parity)) dead = true;  // and no copy is issued any more
+        dead = __any_sync(0xffffffffu, dead);
+        if (!(flags & kDescSkip) && !dead) {
+            const uint8_t* rec = ring + (size_t)stage * rec_bytes;
+            const uint8_t* vpart = rec + 4 * D * a.pg.kb + 2 * D;
+            float s[2][NT][4];
+            switch (a.pg.kb) {
+#define QG_SCORES(B)                                                \
+    case B:                                                         \
+        scores_half<D, NT, B>(rec, 0, lane, q, s[0]);               \
+        scores_half<D, NT, B>(rec, 1, lane, q, s[1]);               \
+        break;
+                QG_SCORES(2)
+                QG_SCORES(3)
+                QG_SCORES(4)
+                QG_SCORES(5)
+                QG_SCORES(6)
+                QG_SCORES(8)
+#undef QG_SCORES
+            }
+            const int t_first = (cs.t0 + d.w) * kTileTokens;
+            const bool masked = t_first + kTileTokens - 1 > lo_pos || (a.window > 0 && t_first <= hi_pos - a.window);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        float x = s[h][nt][c] * q.f[nt][c & 1];
+                        if (masked) {
+                            const int t = t_first + 16 * h + 8 * (c >> 1) + r8, pos = qpos[nt][c & 1];
+                            if (t > pos || (a.window > 0 && t <= pos - a.window)) x = -INFINITY;
+                        }
+                        s[h][nt][c] = x;
+                    }
+            // the running maximum is moved when a score has passed it by more than the slack
+            float tm[NT][2];
+            bool over = false;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    tm[nt][c] = fmaxf(fmaxf(s[0][nt][c], s[0][nt][c + 2]), fmaxf(s[1][nt][c], s[1][nt][c + 2]));
+                    over |= tm[nt][c] > m[nt][c] + kAttSlack;
+                }
+            if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        float t = tm[nt][c];
+#pragma unroll
+                        for (int o = 4; o < 32; o <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, o));
+                        const float mn = fmaxf(m[nt][c], t);
+                        const float k = m[nt][c] == mn ? 1.f : ex2(m[nt][c] - mn);
+                        m[nt][c] = mn;
+                        l[nt][c] *= k;
+#pragma unroll
+                        for (int i = 0; i < 2 * G; ++i) {
+                            acc[nt][i][c] *= k;
+                            acc[nt][i][c + 2] *= k;
+                        }
+                    }
+            }
+            uint32_t p[2][NT][2], on[2][NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const float m0 = (m[nt][0] == -INFINITY ? 0.f : m[nt][0]) - kAttShift;
+                const float m1 = (m[nt][1] == -INFINITY ? 0.f : m[nt][1]) - kAttShift;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const float p0 = ex2(s[h][nt][0] - m0), p1 = ex2(s[h][nt][1] - m1);
+                    const float p2 = ex2(s[h][nt][2] - m0), p3 = ex2(s[h][nt][3] - m1);
+                    l[nt][0] += p0 + p2;
+                    l[nt][1] += p1 + p3;
+                    p[h][nt][0] = movm_trans(h2_bits(__floats2half2_rn(p0, p1)));
+                    p[h][nt][1] = movm_trans(h2_bits(__floats2half2_rn(p2, p3)));
+                    on[h][nt][0] = on[h][nt][1] = 0xffffffffu;
+                }
+            }
+            if (masked) {  // a weight of 0 is 0 whatever the scale it meets
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int k = 0; k < 2; ++k)
+                            on[h][nt][k] = __hneu2_mask(bits_h2(p[h][nt][k]), bits_h2(0));
+            }
+            // V scales are brought below 2 by 2^-E2 of the largest seen
+            __half2 es = __float2half2_rn(__uint_as_float((uint32_t)(127 - E2) << 23));
+            const __half2 vm = __hmul2(v_scale_max<D>(vpart, a.pg.vb, lane, hi_pos - t_first), es);
+            const bool big = __low2float(vm) >= 2.f || __high2float(vm) >= 2.f;
+            if (__any_sync(0xffffffffu, big)) {
+                const __half2 v = v_scale_max<D>(vpart, a.pg.vb, lane, hi_pos - t_first);
+                float t = fmaxf(__low2float(v), __high2float(v));
+                t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
+                t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
+                const int en = min(max((int)(__float_as_uint(t) >> 23) - 127, E2), 15);
+                const float k = __uint_as_float((uint32_t)(127 + E2 - en) << 23);
+                E2 = en;
+                es = __float2half2_rn(__uint_as_float((uint32_t)(127 - E2) << 23));
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int i = 0; i < 2 * G; ++i)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) acc[nt][i][c] *= k;
+            }
+            switch (a.pg.vb) {
+#define QG_OUTPUT(B)                                                                  \
+    case B:                                                                           \
+        output_half<D, NT, B>(vpart, 0, lane, es, p[0], on[0], acc);                  \
+        output_half<D, NT, B>(vpart, 1, lane, es, p[1], on[1], acc);                  \
+        break;
+                QG_OUTPUT(2)
+                QG_OUTPUT(3)
+                QG_OUTPUT(4)
+                QG_OUTPUT(5)
+                QG_OUTPUT(6)
+                QG_OUTPUT(8)
+#undef QG_OUTPUT
+            }
+        }
+        __syncwarp();
+        ++done;
+        --in_flight;
+        if (left > 0) {
+            issue(stage);
+            ++in_flight;
+        }
+        if (flags & kDescLast) {
+            // this warp's part of the item is done: its slot, in the sums' own units
+            // (one that began before this warp is its first, and may leave copies in flight;
+            // one that goes on behind it is its last, and finds the ring drained)
+            float* slot = frag_head ? reinterpret_cast<float*>(ring) : slots + warp * C::SlotFloats;
+            AttFrag& fr = frags[warp * 2 + (frag_head ? 1 : 0)];
+            float unit[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                unit[i] = __uint_as_float((uint32_t)(127 + 24 + E2 - field_at(a.pg.vb, i)) << 23);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+#pragma unroll
+                    for (int o = 4; o < 32; o <<= 1) l[nt][c] += __shfl_xor_sync(0xffffffffu, l[nt][c], o);
+                }
+            if (frag_head && (flags & kDescTail)) {
+                // the whole item: rotate back in this layout (dim 32 g + 4 r + i) and store
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        float x[G][4];
+#pragma unroll
+                        for (int g = 0; g < G; ++g)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) x[g][i] = acc[nt][2 * g + (i >> 1)][(i & 1) * 2 + c] * unit[i];
+#pragma unroll
+                        for (int g = 0; g < G; ++g) {
+#pragma unroll
+                            for (int st = 1; st < 4; st <<= 1)
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    if (!(i & st)) {
+                                        const float u = x[g][i], v = x[g][i + st];
+                                        x[g][i] = u + v;
+                                        x[g][i + st] = u - v;
+                                    }
+#pragma unroll
+                            for (int ls = 4; ls < 32; ls <<= 1)
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) {
+                                    const float o = __shfl_xor_sync(0xffffffffu, x[g][i], ls);
+                                    x[g][i] = (lane & ls) ? o - x[g][i] : x[g][i] + o;
+                                }
+                        }
+#pragma unroll
+                        for (int st = 1; st < G; st <<= 1)
+#pragma unroll
+                            for (int g = 0; g < G; ++g)
+                                if (!(g & st))
+#pragma unroll
+                                    for (int i = 0; i < 4; ++i) {
+                                        const float u = x[g][i], v = x[g + st][i];
+                                        x[g][i] = u + v;
+                                        x[g + st][i] = u - v;
+                                    }
+                        const int r = d.z * RB + 8 * nt + 2 * j + c;
+                        if (r < cs.n * a.group) {
+                            const int tok = r / a.group, hq = head * a.group + (r - tok * a.group);
+                            const float inv = l[nt][c] == 0.f ? 0.f : 1.f / (l[nt][c] * (float)D);
+                            uint16_t* o = reinterpret_cast<uint16_t*>(a.out.p) + (cs.row0 + tok) * a.out.row +
+                                          hq * a.out.head + 4 * r8;
+#pragma unroll
+                            for (int g = 0; g < G; ++g) {
+                                uint16_t v[4];
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) v[i] = kv_from_float<BF16>(x[g][i] * inv);
+                                *reinterpret_cast<uint2*>(o + 32 * g) =
+                                    make_uint2(v[0] | (uint32_t)v[1] << 16, v[2] | (uint32_t)v[3] << 16);
+                            }
+                            if (a.lse && r8 == 0)
+                                a.lse[(int64_t)(cs.row0 + tok) * a.q_heads + hq] =
+                                    (m[nt][c] + log2f(l[nt][c]) - kAttShift) * 0.6931471805599453f;
+                        }
+                    }
+            } else {
+                __syncwarp();
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const int r = 8 * nt + 2 * j + c;
+#pragma unroll
+                        for (int g = 0; g < G; ++g)
+                            *reinterpret_cast<float4*>(slot + r * C::OS + 32 * g + 4 * r8) =
+                                make_float4(acc[nt][2 * g][c] * unit[0], acc[nt][2 * g][c + 2] * unit[1],
+                                            acc[nt][2 * g + 1][c] * unit[2], acc[nt][2 * g + 1][c + 2] * unit[3]);
+                        if (r8 == 0) {
+                            slot[RB * C::OS + r] = m[nt][c];
+                            slot[RB * C::OS + RB + r] = l[nt][c];
+                        }
+                    }
+                if (lane == 0) {
+                    // the item's first tile as a number of the call: this tile's less its place
+                    fr.item = w0 + done - 1 - d.w;
+                    fr.seq = d.x;
+                    fr.head = head;
+                    fr.rb = d.z;
+                    fr.tiles = cs.tiles;
+                }
+            }
+        }
+        if (++stage == a.stages) {
+            stage = 0;
+            parity ^= 1;
+        }
+    }
+    __syncthreads();
+
+    // ---- join: fragments lie in order (warp, slot); those of one item are neighbours
+    int gi = 0;  // groups seen, to deal rows out to warps
+    for (int f = 0; f < 2 * W;) {
+        const AttFrag fr = frags[f];
+        if (fr.tiles == 0) {
+            ++f;
+            continue;
+        }
+        int e = f + 1;
+        while (e < 2 * W && (frags[e].tiles == 0 || frags[e].item == fr.item)) ++e;
+        const bool whole = fr.item >= cta0 && fr.item + fr.tiles <= cta1;
+        const AttSeq s = att_seq<RB>(a, fr.seq);
+        const int rows = min(RB, s.n * a.group - fr.rb * RB);
+        float* gslot = a.partial + ((size_t)blockIdx.x * 2 + (fr.item < cta0 ? 0 : 1)) * C::GSlot;
+        for (int r = 0; r < rows; ++r) {
+            if ((gi * RB + r) % W != warp) continue;
+            float mx = -INFINITY, lt = 0.f, o[E];
+            for (int k = f; k < e; ++k) {
+                if (frags[k].tiles == 0) continue;
+                const float* sl = (k & 1) ? reinterpret_cast<const float*>(rings + (size_t)(k >> 1) * a.stages * rec_bytes)
+                                          : slots + (k >> 1) * C::SlotFloats;
+                mx = fmaxf(mx, sl[RB * C::OS + r]);
+            }
+#pragma unroll
+            for (int i = 0; i < E; ++i) o[i] = 0.f;
+            for (int k = f; k < e; ++k) {
+                if (frags[k].tiles == 0) continue;
+                const float* sl = (k & 1) ? reinterpret_cast<const float*>(rings + (size_t)(k >> 1) * a.stages * rec_bytes)
+                                          : slots + (k >> 1) * C::SlotFloats;
+                const float ms = sl[RB * C::OS + r], w = ms == mx ? 1.f : ex2(ms - mx);
+                lt = fmaf(w, sl[RB * C::OS + RB + r], lt);
+#pragma unroll
+                for (int i = 0; i < E; ++i) o[i] = fmaf(w, sl[r * C::OS + E * lane + i], o[i]);
+            }
+            if (whole) {
+                store_row<D, BF16>(a, o, mx, lt, s.row0, fr.rb * RB + r, fr.head, lane);
+            } else {
+#pragma unroll
+                for (int i = 0; i < E; ++i) gslot[r * D + E * lane + i] = o[i];
+                if (lane == 0) {
+                    gslot[RB * D + r] = mx;
+                    gslot[RB * D + RB + r] = lt;
+                }
+            }
+        }
+        if (!whole) {
+            // the last CTA of the item to get here joins them, first to last
+            const int c0 = (int)(fr.item / share), c1 = (int)((fr.item + fr.tiles - 1) / share);
+            __threadfence();
+            __syncthreads();
+            if (threadIdx.x == 0) {
+                const bool last = atomicAdd(&a.tickets[c0], 1u) == (unsigned)(c1 - c0);
+                if (last) a.tickets[c0] = 0;
+                __threadfence();
+                sh_last = last;
+            }
+            __syncthreads();
+            if (sh_last) {
+                for (int r = warp; r < rows; r += W) {
+                    float mx = -INFINITY, lt = 0.f, o[E];
+                    for (int k = c0 + lane; k <= c1; k += 32)
+                        mx = fmaxf(mx, __ldcg(a.partial + ((size_t)k * 2 + (k == c0 ? 1 : 0)) * C::GSlot + RB * D + r));
+#pragma unroll
+                    for (int o2 = 1; o2 < 32; o2 <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o2));
+#pragma unroll
+                    for (int i = 0; i < E; ++i) o[i] = 0.f;
+                    for (int k = c0; k <= c1; ++k) {
+                        const float* sl = a.partial + ((size_t)k * 2 + (k == c0 ? 1 : 0)) * C::GSlot;
+                        const float ms = __ldcg(sl + RB * D + r), w = ms == mx ? 1.f : ex2(ms - mx);
+                        lt = fmaf(w, __ldcg(sl + RB * D + RB + r), lt);
+#pragma unroll
+                        for (int i = 0; i < E; ++i) o[i] = fmaf(w, __ldcg(sl + r * D + E * lane + i), o[i]);
+                    }
+                    store_row<D, BF16>(a, o, mx, lt, s.row0, fr.rb * RB + r, fr.head, lane);
+                }
+            }
+        }
+        ++gi;
+        f = e;
+    }
+}
+
+}  // namespace qg

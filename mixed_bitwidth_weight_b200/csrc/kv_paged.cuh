@@ -265,112 +265,4 @@ __global__ void __launch_bounds__(32 * kKvWarps) kv_gather_kernel(KvPages pg, Kv
     for (int i = 0; i < E; ++i) p[i] = kv_from_float<BF16>(__fmul_rn(x[i], 1.f / (float)D));
 }
 
-// ------------------------------------------------------------------- attend
-struct KvAttend {
-    KvPages pg;
-    KvBatch bt;
-    KvRows q, out;
-    float* lse;  // [rows][q_heads] or null
-    int q_heads, window;
-    float scale;
-};
-
-constexpr int kAttRows = 8;
-
-// One CTA per (sequence, KV head); rows (query token, head of the group) in
-// blocks of 8.  Each warp takes every eighth token with its own running
-// maximum and sum; the warps are joined at the end.  Works on the rotated
-// values: q . k' = (H q) . u / D, and the sum of p v' is H (sum of p u) / D.
-template <int D, bool BF16>
-__global__ void __launch_bounds__(32 * kKvWarps) kv_attend_kernel(KvAttend a) {
-    constexpr int E = D / 32;
-    __shared__ uint8_t sh_codes[kKvWarps][D];
-    __shared__ float sh_acc[kKvWarps][D];
-    __shared__ float sh_m[kKvWarps], sh_l[kKvWarps];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int b = blockIdx.y, head = blockIdx.x, group = a.q_heads / a.pg.heads;
-    const int row0 = a.bt.cu[b], n = min(a.bt.cu[b + 1], a.bt.rows) - row0, len = a.bt.lens[b];
-    if (row0 < 0 || n <= 0) return;
-    const int rb = kv_record_bytes<D>(a.pg.kb, a.pg.vb);
-    for (int r0 = 0; r0 < n * group; r0 += kAttRows) {
-        float qf[kAttRows][E], acc[kAttRows][E], m[kAttRows], l[kAttRows];
-#pragma unroll
-        for (int r = 0; r < kAttRows; ++r) {
-            m[r] = -INFINITY;
-            l[r] = 0.f;
-#pragma unroll
-            for (int i = 0; i < E; ++i) qf[r][i] = acc[r][i] = 0.f;
-            if (r0 + r < n * group) {
-                const int tok = (r0 + r) / group, hq = head * group + (r0 + r) % group;
-                const uint16_t* p = reinterpret_cast<const uint16_t*>(a.q.p) + (row0 + tok) * a.q.row +
-                                    hq * a.q.head + E * lane;
-#pragma unroll
-                for (int i = 0; i < E; ++i) qf[r][i] = kv_to_float<BF16>(p[i]);
-                fwht_warp<E>(qf[r], lane);
-#pragma unroll
-                for (int i = 0; i < E; ++i) qf[r][i] *= a.scale / (float)D;
-            }
-        }
-        const int first_pos = len - n + r0 / group;
-        const int last_pos = len - n + (min(r0 + kAttRows, n * group) - 1) / group;
-        const int t0 = a.window > 0 ? max(0, first_pos - a.window + 1) : 0;
-        for (int t = t0 + warp; t <= last_pos; t += kKvWarps) {
-            const uint8_t* rec = kv_record(a.pg, a.bt, b, t, head, rb);
-            if (!rec) continue;
-            float x[E], y[E];
-            kv_load_token<D, true>(rec, t & 31, a.pg.kb, a.pg.vb, sh_codes[warp], lane, x);
-            kv_load_token<D, false>(rec, t & 31, a.pg.kb, a.pg.vb, sh_codes[warp], lane, y);
-#pragma unroll
-            for (int r = 0; r < kAttRows; ++r) {
-                float s = 0.f;
-#pragma unroll
-                for (int i = 0; i < E; ++i) s += qf[r][i] * x[i];
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-                const int pos = len - n + (r0 + r) / group;
-                if (t > pos || (a.window > 0 && t <= pos - a.window)) continue;
-                const float mn = fmaxf(m[r], s);
-                const float c = m[r] == mn ? 1.f : expf(m[r] - mn), p = s == mn ? 1.f : expf(s - mn);
-                m[r] = mn;
-                l[r] = l[r] * c + p;
-#pragma unroll
-                for (int i = 0; i < E; ++i) acc[r][i] = acc[r][i] * c + p * y[i];
-            }
-        }
-#pragma unroll
-        for (int r = 0; r < kAttRows; ++r) {
-            if (r0 + r >= n * group) break;
-            __syncthreads();
-            if (lane == 0) {
-                sh_m[warp] = m[r];
-                sh_l[warp] = l[r];
-            }
-#pragma unroll
-            for (int i = 0; i < E; ++i) sh_acc[warp][E * lane + i] = acc[r][i];
-            __syncthreads();
-            if (warp == r) {
-                float mx = -INFINITY, lt = 0.f, o[E];
-                for (int w = 0; w < kKvWarps; ++w) mx = fmaxf(mx, sh_m[w]);
-#pragma unroll
-                for (int i = 0; i < E; ++i) o[i] = 0.f;
-                for (int w = 0; w < kKvWarps; ++w) {
-                    const float c = sh_m[w] == mx ? 1.f : expf(sh_m[w] - mx);
-                    lt += c * sh_l[w];
-#pragma unroll
-                    for (int i = 0; i < E; ++i) o[i] += c * sh_acc[w][E * lane + i];
-                }
-                fwht_warp<E>(o, lane);
-                const int tok = (r0 + r) / group, hq = head * group + (r0 + r) % group;
-                uint16_t* p = reinterpret_cast<uint16_t*>(a.out.p) + (row0 + tok) * a.out.row + hq * a.out.head +
-                              E * lane;
-                const float inv = lt == 0.f ? 0.f : 1.f / (lt * (float)D);
-#pragma unroll
-                for (int i = 0; i < E; ++i) p[i] = kv_from_float<BF16>(o[i] * inv);
-                if (a.lse && lane == 0) a.lse[(int64_t)(row0 + tok) * a.q_heads + hq] = mx + logf(lt);
-            }
-        }
-        __syncthreads();
-    }
-}
-
 }  // namespace qg

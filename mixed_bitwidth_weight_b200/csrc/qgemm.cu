@@ -18,6 +18,7 @@
 #include "quantize.cuh"
 #include "kv_cache.cuh"
 #include "kv_paged.cuh"
+#include "kv_attend.cuh"
 
 namespace {
 
@@ -31,6 +32,7 @@ struct DeviceInfo {
     bool int_attr[3] = {false, false, false};
     bool gemm_attr[2] = {false, false};
     bool quant_attr = false;
+    bool attend_attr[3][2][2] = {};  // [head size][row tiles][bf16]
 };
 
 DeviceInfo g_devs[64];
@@ -936,6 +938,40 @@ int kv_move(bool append, const qgemm_kv_cache* cache, const qgemm_kv_batch* batc
     return launch_status();
 }
 
+// Row tiles of the attention kernel: two (16 query rows an item) when a
+// sequence brings more than 8 rows on average, except for 256 dims, whose
+// accumulators for 16 rows would not fit the registers.
+int attend_row_tiles(int D, int64_t rows, int num_seqs, int group) {
+    if (D == 256) return 1;
+    return (rows + num_seqs - 1) / num_seqs * group > 8 ? 2 : 1;
+}
+
+constexpr size_t kAttendTicketBytes = 1024;  // one counter per CTA
+
+size_t attend_ws_bytes(int D, int sms) {
+    const size_t rows = D == 256 ? 8 : 16;
+    return kAttendTicketBytes + (size_t)sms * 2 * rows * (D + 2) * 4;
+}
+
+template <int D, int NT, bool BF16>
+int launch_attend(KvAttend a, DeviceInfo* dev, bool* attr, cudaStream_t s) {
+    using C = AttCfg<D, NT>;
+    constexpr size_t most = 226 * 1024;  // 227 KB a CTA, some of it static
+    const size_t rec = (size_t)4 * D * (a.pg.kb + a.pg.vb + 1);
+    a.stages = (int)std::min<size_t>(kAttMaxStages, (most - C::RingAt) / (C::W * rec));
+    if (a.stages < 1 || a.stages * rec < (size_t)C::SlotBytes) return QGEMM_ERR_UNSUPPORTED;
+    if (!*attr) {  // a per-device setting
+        if (cudaFuncSetAttribute(kv_attend_kernel<D, NT, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)most) != cudaSuccess) {
+            cudaGetLastError();
+            return QGEMM_ERR_CUDA;
+        }
+        *attr = true;
+    }
+    kv_attend_kernel<D, NT, BF16><<<dev->sms, 32 * C::W, C::RingAt + C::W * a.stages * rec, s>>>(a);
+    return launch_status();
+}
+
 }  // namespace
 
 // =========================================================== C ABI
@@ -1304,7 +1340,7 @@ size_t qgemm_kv_attend_workspace_bytes(const qgemm_kv_cache* c, int q_heads) {
     if (!c || check_kv_geometry(c->kv_heads, c->head_dim, c->k_bits, c->v_bits, c->page_size) != QGEMM_OK ||
         q_heads < 1 || q_heads % c->kv_heads)
         return 0;
-    return 16;
+    return attend_ws_bytes(c->head_dim, device_sms());
 }
 
 int qgemm_kv_attend(const qgemm_kv_cache* cache, const qgemm_kv_batch* batch, int num_rows, const void* d_q, int64_t q_row_stride,
@@ -1328,14 +1364,26 @@ int qgemm_kv_attend(const qgemm_kv_cache* cache, const qgemm_kv_batch* batch, in
     a.q_heads = q_heads;
     a.window = window;
     a.scale = scale;
-    const dim3 grid(a.pg.heads, a.bt.num_seqs);
+    DeviceInfo* dev = nullptr;
+    if ((st = current_device_info(&dev)) != QGEMM_OK) return st;
+    if (ws_bytes < attend_ws_bytes(D, dev->sms) || dev->sms > (int)(kAttendTicketBytes / 4)) return QGEMM_ERR_WORKSPACE;
+    a.group = q_heads / a.pg.heads;
+    a.tickets = static_cast<unsigned int*>(d_ws);
+    a.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(d_ws) + kAttendTicketBytes);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool bf = dtype == QGEMM_BF16;
-    auto f = D == 64 ? (bf ? kv_attend_kernel<64, true> : kv_attend_kernel<64, false>)
-             : D == 128 ? (bf ? kv_attend_kernel<128, true> : kv_attend_kernel<128, false>)
-                        : (bf ? kv_attend_kernel<256, true> : kv_attend_kernel<256, false>);
-    f<<<grid, 32 * kKvWarps, 0, s>>>(a);
-    return launch_status();
+    const int nt = attend_row_tiles(D, a.bt.rows, a.bt.num_seqs, a.group);
+#define QG_ATTEND(DD, NT, I)                                                                  \
+    if (D == DD && nt == NT)                                                                  \
+        return bf ? launch_attend<DD, NT, true>(a, dev, &dev->attend_attr[I][NT - 1][1], s)   \
+                  : launch_attend<DD, NT, false>(a, dev, &dev->attend_attr[I][NT - 1][0], s);
+    QG_ATTEND(64, 1, 0)
+    QG_ATTEND(64, 2, 0)
+    QG_ATTEND(128, 1, 1)
+    QG_ATTEND(128, 2, 1)
+    QG_ATTEND(256, 1, 2)
+#undef QG_ATTEND
+    return QGEMM_ERR_UNSUPPORTED;
 }
 
 size_t qgemm_noalloc_scratch_bytes(int M, int K, int N) {
