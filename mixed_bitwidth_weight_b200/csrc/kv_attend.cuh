@@ -45,7 +45,8 @@ struct KvAttend {
     KvBatch bt;
     KvRows q, out;
     float* lse;  // [rows][q_heads] or null
-    int32_t q_heads, group, window, stages;
+    int32_t q_heads, group, window;
+    int32_t stages, stage_bytes, ring_bytes;  // of a warp's ring
     float scale;
     unsigned int* tickets;  // [CTAs], zero between calls
     float* partial;         // [CTAs][2] slots
@@ -57,18 +58,25 @@ constexpr float kAttSlack = 4.f;     // the running maximum may be this far behi
 
 template <int D, int NT>
 struct AttCfg {
-    static constexpr int W = D * NT <= 128 ? 16 : 8;  // warps
+    static constexpr int W = 8;                       // warps: 255 registers a thread, nothing spilled
     static constexpr int G = D / 32;
     static constexpr int RB = 8 * NT;                 // query rows of an item
     static constexpr int OS = D + 4;                  // row stride of a slot: conflict-free float4 stores
     static constexpr int SlotFloats = RB * OS + 2 * RB;
     static constexpr int SlotBytes = SlotFloats * 4;
     static constexpr int GSlot = RB * D + 2 * RB;     // floats of a global slot
-    // shared memory: slots, stage descriptors, barriers, fragments, rings
-    static constexpr int DescAt = W * SlotBytes;
+    // an item's rotated query: [nt][g][hi, lo][lane] 16 bytes, then zq [nt][g][8], f [nt][8]
+    static constexpr int QZero = NT * G * 256, QFactor = QZero + NT * G * 8;
+    static constexpr int QFloats = QFactor + NT * 8, QBytes = QFloats * 4;
+    // shared memory: slots, query areas, stage descriptors, barriers, fragments, rings
+    static constexpr int QAt = W * SlotBytes;
+    static constexpr int DescAt = QAt + W * QBytes;
     static constexpr int BarAt = DescAt + W * 8 * 16;
     static constexpr int FragAt = BarAt + W * 8 * 8;
     static constexpr int RingAt = (FragAt + 2 * W * 24 + 127) / 128 * 128;
+    // the join's weights and row buffer lie over the query areas
+    static constexpr int MaxCtas = 160;
+    static_assert(W * QBytes >= (RB * MaxCtas + RB * D + 2 * RB) * 4, "join buffers");
 };
 
 // a slot's fragment: tiles [a, b) of the item whose first tile is number `item`
@@ -83,6 +91,15 @@ QG_DEV void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// the first of a chain: starts at (c0, c1) for both row halves
+QG_DEV void mma_f16_from(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1,
+                         float c0, float c1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%10,%11};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1));
 }
 
 QG_DEV uint32_t movm_trans(uint32_t a) {
@@ -231,10 +248,6 @@ QG_DEV void scores_half(const uint8_t* rec, int half, int lane, const AttQ<D, NT
         }
     }
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) s[nt][i] = 0.f;
-#pragma unroll
     for (int g = 0; g < G; ++g) {
         const int p0 = g * 8 * B, p1 = (G + g) * 8 * B;  // units of the two tokens
         uint32_t a[8];
@@ -263,122 +276,107 @@ QG_DEV void scores_half(const uint8_t* rec, int half, int lane, const AttQ<D, NT
         const float s1 = (g & 1) ? __high2float(h1) : __low2float(h1);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            float c[4] = {q.zq[nt][g][0], q.zq[nt][g][1], q.zq[nt][g][0], q.zq[nt][g][1]};
-            mma_f16(c, a[0], a[1], a[2], a[3], q.hi[nt][g][0], q.hi[nt][g][1]);
+            float c[4];
+            mma_f16_from(c, a[0], a[1], a[2], a[3], q.hi[nt][g][0], q.hi[nt][g][1], q.zq[nt][g][0], q.zq[nt][g][1]);
             mma_f16(c, a[4], a[5], a[6], a[7], q.hi[nt][g][2], q.hi[nt][g][3]);
             mma_f16(c, a[0], a[1], a[2], a[3], q.lo[nt][g][0], q.lo[nt][g][1]);
             mma_f16(c, a[4], a[5], a[6], a[7], q.lo[nt][g][2], q.lo[nt][g][3]);
-            s[nt][0] = fmaf(c[0], s0, s[nt][0]);
-            s[nt][1] = fmaf(c[1], s0, s[nt][1]);
-            s[nt][2] = fmaf(c[2], s1, s[nt][2]);
-            s[nt][3] = fmaf(c[3], s1, s[nt][3]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float si = i < 2 ? s0 : s1;
+                s[nt][i] = g == 0 ? c[i] * si : fmaf(c[i], si, s[nt][i]);
+            }
         }
     }
 }
 
-// Rotate this warp's query rows (lane 4 n + j: row n's dims 32 g + 8 j + i) and
-// split them.  Butterflies in fp32: strides 1, 2, 4 within the lane, 8 and 16
-// between the four lanes of a row, the rest within the lane.
+// Rotate query row n (of 8) of row tile nt, a warp to a row, split it into its two
+// parts and put them where the B operand's lanes read them (row n's dims
+// 32 g + 8 j + i are lane 4 n + j's, pair i % 4, half i / 4).  p: the row, or null.
 template <int D, int NT, bool BF16>
-QG_DEV void load_queries(const KvAttend& a, int row0, int rows, int r_base, int head, int lane, AttQ<D, NT>& q) {
-    constexpr int G = D / 32;
+QG_DEV void rotate_query(const KvAttend& a, const uint16_t* p, float* area, int nt, int n, int lane) {
+    using C = AttCfg<D, NT>;
+    constexpr int E = D / 32, G = D / 32;
+    float x[E];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-        const int j = lane & 3, r = r_base + nt * 8 + (lane >> 2);
-        float x[G][8];
-        if (r < rows) {
-            const int tok = r / a.group, hq = head * a.group + (r - tok * a.group);
-            const uint16_t* p = reinterpret_cast<const uint16_t*>(a.q.p) + (row0 + tok) * a.q.row + hq * a.q.head;
-#pragma unroll
-            for (int g = 0; g < G; ++g) {
-                const uint4 u = __ldg(reinterpret_cast<const uint4*>(p + 32 * g + 8 * j));
-                const uint32_t v[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    x[g][i] = kv_to_float<BF16>((uint16_t)((i & 1) ? v[i / 2] >> 16 : v[i / 2] & 0xffff));
-            }
+    for (int i = 0; i < E; ++i) x[i] = 0.f;
+    if (p) {
+        uint16_t v[E];
+        if constexpr (E == 2) {
+            *reinterpret_cast<uint32_t*>(v) = __ldg(reinterpret_cast<const uint32_t*>(p + 2 * lane));
         } else {
 #pragma unroll
-            for (int g = 0; g < G; ++g)
-#pragma unroll
-                for (int i = 0; i < 8; ++i) x[g][i] = 0.f;
-        }
-#pragma unroll
-        for (int g = 0; g < G; ++g) {
-#pragma unroll
-            for (int st = 1; st < 8; st <<= 1)
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (!(i & st)) {
-                        const float u = x[g][i], v = x[g][i + st];
-                        x[g][i] = u + v;
-                        x[g][i + st] = u - v;
-                    }
-#pragma unroll
-            for (int ls = 1; ls < 4; ls <<= 1)
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float o = __shfl_xor_sync(0xffffffffu, x[g][i], ls);
-                    x[g][i] = (lane & ls) ? o - x[g][i] : x[g][i] + o;
-                }
-        }
-#pragma unroll
-        for (int st = 1; st < G; st <<= 1)
-#pragma unroll
-            for (int g = 0; g < G; ++g)
-                if (!(g & st))
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float u = x[g][i], v = x[g + st][i];
-                        x[g][i] = u + v;
-                        x[g + st][i] = u - v;
-                    }
-        // largest magnitude into [2^14, 2^15): both fp16 parts keep their bits
-        float amax = 0.f;
-#pragma unroll
-        for (int g = 0; g < G; ++g)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(x[g][i]));
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-        int e = (int)(__float_as_uint(amax) >> 23) - 127;  // 128 for infinity: no scaling then
-        e = e >= 128 ? 14 : max(e, -100);
-        const float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
-        const float f = a.scale * (1.4426950408889634f / (float)D) * 16777216.f *
-                        __uint_as_float((uint32_t)(127 - 14 + e) << 23);
-        float dn[4];  // what pair i's place in its word multiplies a code by
-#pragma unroll
-        for (int i = 0; i < 4; ++i) dn[i] = __uint_as_float((uint32_t)(127 - field_at(a.pg.kb, i)) << 23);
-        const float z = (float)(1 << (a.pg.kb - 1)) * 5.9604644775390625e-8f;
-        const int src = (lane & 3) * 8;  // lane of row 2j (4 * 2j)
-#pragma unroll
-        for (int g = 0; g < G; ++g) {
-            float sum = 0.f;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float u = x[g][i] * up, v = x[g][i + 4] * up, ud = u * dn[i], vd = v * dn[i];
-                const __half2 hi = __floats2half2_rn(ud, vd);
-                const __half2 lo = __floats2half2_rn(ud - __low2float(hi), vd - __high2float(hi));
-                q.hi[nt][g][i] = h2_bits(hi);
-                q.lo[nt][g][i] = h2_bits(lo);
-                sum += u + v;
+            for (int i = 0; i < E; i += 4) {
+                const uint2 u = __ldg(reinterpret_cast<const uint2*>(p + E * lane + i));
+                v[i] = (uint16_t)u.x;
+                v[i + 1] = (uint16_t)(u.x >> 16);
+                v[i + 2] = (uint16_t)u.y;
+                v[i + 3] = (uint16_t)(u.y >> 16);
             }
-            sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-            sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-            q.zq[nt][g][0] = -z * __shfl_sync(0xffffffffu, sum, src);
-            q.zq[nt][g][1] = -z * __shfl_sync(0xffffffffu, sum, src + 4);
         }
-        q.f[nt][0] = __shfl_sync(0xffffffffu, f, src);
-        q.f[nt][1] = __shfl_sync(0xffffffffu, f, src + 4);
+#pragma unroll
+        for (int i = 0; i < E; ++i) x[i] = kv_to_float<BF16>(v[i]);
+    }
+    fwht_warp<E>(x, lane);
+    // largest magnitude into [2^14, 2^15): both fp16 parts keep their bits
+    float amax = 0.f;
+#pragma unroll
+    for (int i = 0; i < E; ++i) amax = fmaxf(amax, fabsf(x[i]));
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    int e = (int)(__float_as_uint(amax) >> 23) - 127;  // 128 for infinity: no scaling then
+    e = e >= 128 ? 14 : max(e, -100);
+    const float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
+    uint16_t* out = reinterpret_cast<uint16_t*>(area);
+    float sum = 0.f;
+    const int g = E * lane / 32;
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+        const int d = E * lane + i, pair = d & 3;
+        const float v = x[i] * up, vd = v * __uint_as_float((uint32_t)(127 - field_at(a.pg.kb, pair)) << 23);
+        const __half hi = __float2half_rn(vd), lo = __float2half_rn(vd - __half2float(hi));
+        const int at = ((((nt * G + g) * 2) * 32 + 4 * n + ((d & 31) >> 3)) * 4 + pair) * 2 + ((d >> 2) & 1);
+        out[at] = __half_as_ushort(hi);
+        out[at + 32 * 8] = __half_as_ushort(lo);
+        sum += v;
+    }
+#pragma unroll
+    for (int o = 1; o < 32 / E; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane % (32 / E) == 0)
+        area[C::QZero + (nt * G + g) * 8 + n] = -(float)(1 << (a.pg.kb - 1)) * 5.9604644775390625e-8f * sum;
+    if (lane == 0)
+        area[C::QFactor + nt * 8 + n] = a.scale * (1.4426950408889634f / (float)D) * 16777216.f *
+                                        __uint_as_float((uint32_t)(127 - 14 + e) << 23);
+}
+
+template <int D, int NT>
+QG_DEV void load_queries(const float* area, int lane, AttQ<D, NT>& q) {
+    using C = AttCfg<D, NT>;
+    constexpr int G = D / 32;
+    const uint4* f = reinterpret_cast<const uint4*>(area);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+            const uint4 h = f[((nt * G + g) * 2) * 32 + lane], l = f[((nt * G + g) * 2 + 1) * 32 + lane];
+            q.hi[nt][g][0] = h.x, q.hi[nt][g][1] = h.y, q.hi[nt][g][2] = h.z, q.hi[nt][g][3] = h.w;
+            q.lo[nt][g][0] = l.x, q.lo[nt][g][1] = l.y, q.lo[nt][g][2] = l.z, q.lo[nt][g][3] = l.w;
+            const float2 z = *reinterpret_cast<const float2*>(area + C::QZero + (nt * G + g) * 8 + 2 * (lane & 3));
+            q.zq[nt][g][0] = z.x;
+            q.zq[nt][g][1] = z.y;
+        }
+        const float2 v = *reinterpret_cast<const float2*>(area + C::QFactor + nt * 8 + 2 * (lane & 3));
+        q.f[nt][0] = v.x;
+        q.f[nt][1] = v.y;
     }
 }
 
 // ------------------------------------------------------------------- output
 // acc += (codes of V) x (weights): half a tile.  p[nt][k]: weights of tokens
-// 16 half + 8 k + 2 j + {0, 1} for row n = lane / 4; on[nt][k] their masks.
+// 16 half + 8 k + 2 j + {0, 1} for row n = lane / 4.
 template <int D, int NT, int B>
-QG_DEV void output_half(const uint8_t* part, int half, int lane, __half2 es, const uint32_t (&p)[NT][2],
-                        const uint32_t (&on)[NT][2], float (&acc)[NT][D / 16][4]) {
+QG_DEV void output_half(const uint8_t* part, int half, int lane, __half2 es, const uint32_t (&p)[NT][2], bool masked,
+                        float (&acc)[NT][D / 16][4]) {
     constexpr int G = D / 32, NW = D * B / 64, UT = D / 64 * 8 * B;  // bits of a token's units
     uint32_t w[NW];
     load_words<D, B>(part, half, lane, w);
@@ -390,8 +388,15 @@ QG_DEV void output_half(const uint8_t* part, int half, int lane, __half2 es, con
         uint32_t b0[NT], b1[NT];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            b0[nt] = h2_bits(__hmul2(bits_h2(p[nt][0]), s0)) & on[nt][0];
-            b1[nt] = h2_bits(__hmul2(bits_h2(p[nt][1]), s1)) & on[nt][1];
+            b0[nt] = h2_bits(__hmul2(bits_h2(p[nt][0]), s0));
+            b1[nt] = h2_bits(__hmul2(bits_h2(p[nt][1]), s1));
+        }
+        if (masked) {  // a weight of 0 is 0 whatever the scale it meets
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                b0[nt] &= __hneu2_mask(bits_h2(p[nt][0]), bits_h2(0));
+                b1[nt] &= __hneu2_mask(bits_h2(p[nt][1]), bits_h2(0));
+            }
         }
         const int unit = (g >> 1) * 8 * B + (g & 1) * 4 * B;  // this group's four codes in a token's units
         uint32_t f[2][4];
@@ -423,31 +428,21 @@ QG_DEV void output_half(const uint8_t* part, int half, int lane, __half2 es, con
     }
 }
 
-// largest V scale among this lane's tokens of the tile, up to slot `last`
+// largest V scale among this lane's share of the tile's, up to token slot `last`
 // (slots behind the last visible token may hold anything)
 template <int D>
 QG_DEV __half2 v_scale_max(const uint8_t* part, int vb, int lane, int last) {
-    constexpr int G = D / 32;
-    const uint8_t* scales = part + 4 * D * vb + (lane & 3) * G * 16;
+    constexpr int G = D / 32, N = D / 64;  // words of a lane, [j][g][tt] in all
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(part + 4 * D * vb) + N * lane;
     __half2 m = bits_h2(0);
-    uint32_t keep[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
-    if (last < kTileTokens - 1) {
 #pragma unroll
-        for (int tt = 0; tt < 4; ++tt) {
-            const int t = 8 * tt + 2 * (lane & 3);
-            keep[tt] = t + 1 <= last ? 0xffffffffu : t <= last ? 0xffffu : 0u;
-        }
-    }
-#pragma unroll
-    for (int g = 0; g < G; ++g) {
-        uint4 u = *reinterpret_cast<const uint4*>(scales + g * 16);
+    for (int i = 0; i < N; ++i) {
+        uint32_t u = w[i];
         if (last < kTileTokens - 1) {
-            u.x &= keep[0];
-            u.y &= keep[1];
-            u.z &= keep[2];
-            u.w &= keep[3];
+            const int at = N * lane + i, t = 8 * (at & 3) + 2 * (at / (4 * G));
+            u &= t + 1 <= last ? 0xffffffffu : t <= last ? 0xffffu : 0u;
         }
-        m = __hmax2(m, __hmax2(__hmax2(bits_h2(u.x), bits_h2(u.y)), __hmax2(bits_h2(u.z), bits_h2(u.w))));
+        m = __hmax2(m, bits_h2(u));
     }
     return m;
 }
@@ -479,6 +474,10 @@ QG_DEV AttSeq att_seq(const KvAttend& a, int b) {
     return s;
 }
 
+QG_DEV long long div_ll(long long a, int b) {
+    return (a >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
 struct AttCursor {
     int b, h, rb, tile;
     AttSeq s;
@@ -504,9 +503,9 @@ QG_DEV void att_seek(const KvAttend& a, const long long* prefix, int nthreads, i
         if (rem < work || c.b + 1 >= a.bt.num_seqs) break;
         rem -= work;
     }
-    const long long item = rem / c.s.tiles;
+    const long long item = div_ll(rem, c.s.tiles);
     c.tile = (int)(rem - item * c.s.tiles);
-    c.h = (int)(item / c.s.nrb);
+    c.h = (int)div_ll(item, c.s.nrb);
     c.rb = (int)(item - (long long)c.h * c.s.nrb);
 }
 
@@ -565,7 +564,8 @@ __global__ void __launch_bounds__(32 * AttCfg<D, NT>::W, 1) kv_attend_kernel(KvA
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::BarAt) + warp * kAttMaxStages;
     AttFrag* frags = reinterpret_cast<AttFrag*>(smem + C::FragAt);
     uint8_t* rings = smem + C::RingAt;
-    uint8_t* ring = rings + (size_t)warp * a.stages * rec_bytes;
+    uint8_t* ring = rings + warp * a.ring_bytes;
+    const int k_bytes = 4 * D * a.pg.kb + 2 * D, v_bytes = rec_bytes - k_bytes;
     long long* prefix = reinterpret_cast<long long*>(smem);  // before the slots are used
 
     // ---- the call's work, and this CTA's and warp's share
@@ -594,55 +594,112 @@ __global__ void __launch_bounds__(32 * AttCfg<D, NT>::W, 1) kv_attend_kernel(KvA
     }
     prefix[threadIdx.x] = before + inc - mine;
     __syncthreads();
-    const long long share = max((total + gridDim.x - 1) / gridDim.x, (long long)W);
+    // two tiles a warp at least: a join across CTAs costs more than a second tile
+    const long long share = max((total + gridDim.x - 1) / gridDim.x, 2ll * W);
     const long long cta0 = min(share * blockIdx.x, total), cta1 = min(cta0 + share, total);
     if (cta0 >= cta1) return;
     const long long per = (cta1 - cta0 + W - 1) / W;
     const long long w0 = min(cta0 + per * warp, cta1), w1 = min(w0 + per, cta1);
-    AttCursor pc;  // the producer's place
+    AttCursor pc, cc;  // the producer's place, and the CTA's first
+    att_seek<RB>(a, prefix, T, chunk, cta0, lane, cc);
     long long left = w1 - w0;
-    if (left > 0) att_seek<RB>(a, prefix, T, chunk, w0, lane, pc);
+    // walk the CTA's items to the warp's; where the CTA has no more than W of
+    // them, all warps share their rotated queries
+    pc = cc;
+    int my_item = 0, items = 0;
+    {
+        AttCursor c = cc;
+        long long at = cta0 - c.tile;
+        for (; items <= W && at < cta1; ++items) {
+            if (w0 >= at && w0 < at + c.s.tiles) {
+                pc = c;
+                pc.tile = (int)(w0 - at);
+                my_item = items;
+            }
+            at += c.s.tiles;
+            c.tile = c.s.tiles - 1;
+            att_next<RB>(a, c, at < cta1);
+        }
+    }
+    const bool shared_q = items <= W;
+    if (!shared_q && left > 0) att_seek<RB>(a, prefix, T, chunk, w0, lane, pc);
     __syncthreads();  // prefix is read; slots may be written
 
     // ---- one warp's run
     const int lps = 31 - __clz(a.pg.page_size / kTileTokens);  // log2 tiles per page
-    int page_base = -1, page_b = -1, page_id = 0;              // lane i: page page_base + i of sequence page_b
-    bool first_of_run = true;
-    bool dead = false;
+    int page_base = 0, page_b = -1, page_id = 0;               // lane i: page page_base + i of sequence page_b
+    int page_left = 0;                                         // tiles of the page still to come
+    bool has = false, first_of_run = true, dead = false;
+    bool value_next = false;  // copies alternate: a tile's K part, its V part
+    const uint8_t* src = nullptr;
     auto issue = [&](int s) {
-        const int T0 = pc.s.t0 + pc.tile;
-        int flags = (first_of_run || pc.tile == 0 ? kDescFirst : 0) | (left == 1 || pc.tile + 1 == pc.s.tiles ? kDescLast : 0) |
-                    (pc.tile == 0 ? kDescHead : 0) | (pc.tile + 1 == pc.s.tiles ? kDescTail : 0);
-        first_of_run = false;
-        const int pi = T0 >> lps;
-        if (page_b != pc.b || pi < page_base || pi >= page_base + 32) {
-            page_b = pc.b;
-            page_base = pi;
-            page_id = pi + lane < a.bt.max_pages && (int64_t)(pi + lane) * a.pg.page_size < pc.s.len
-                          ? a.bt.table[pc.b * a.bt.table_stride + pi + lane]
-                          : -1;
+        if (value_next) {
+            if (lane == 0) {
+                if (has && !dead) {
+                    mbar_arrive_expect_tx(&bars[s], v_bytes);
+                    bulk_g2s(ring + s * a.stage_bytes, src + k_bytes, v_bytes, &bars[s]);
+                } else {
+                    mbar_arrive(&bars[s]);
+                }
+            }
+            value_next = false;
+            src += rec_bytes;
+            --page_left;
+            --left;
+            att_next<RB>(a, pc, left > 0);
+            return;
         }
-        const int page = __shfl_sync(0xffffffffu, page_id, pi - page_base);
-        const bool has = pc.s.len > 0 && page >= 0 && page < a.pg.num_pages && !dead;
-        if (!has) flags |= kDescSkip;
+        if (page_left == 0 || pc.tile == 0) {
+            const int T0 = pc.s.t0 + pc.tile, pi = T0 >> lps;
+            if (page_b != pc.b || pi < page_base || pi >= page_base + 32) {
+                page_b = pc.b;
+                page_base = pi;
+                page_id = pi + lane < a.bt.max_pages && (int64_t)(pi + lane) * a.pg.page_size < pc.s.len
+                              ? a.bt.table[pc.b * a.bt.table_stride + pi + lane]
+                              : -1;
+            }
+            const int page = __shfl_sync(0xffffffffu, page_id, pi - page_base), in = T0 & ((1 << lps) - 1);
+            page_left = (1 << lps) - in;
+            has = pc.s.len > 0 && page >= 0 && page < a.pg.num_pages;
+            if (pc.s.len > 0 && !has && lane == 0) set_dev_error(QGEMM_DEV_BAD_PAGE);
+            src = a.pg.base + page * a.pg.page_bytes + (int64_t)((pc.h << lps) + in) * rec_bytes;
+        }
+        const int flags = (first_of_run || pc.tile == 0 ? kDescFirst : 0) |
+                          (left == 1 || pc.tile + 1 == pc.s.tiles ? kDescLast : 0) | (has ? 0 : kDescSkip) |
+                          (pc.tile == 0 ? kDescHead : 0) | (pc.tile + 1 == pc.s.tiles ? kDescTail : 0);
         if (lane == 0) {
-            if (pc.s.len > 0 && !has && !dead) set_dev_error(QGEMM_DEV_BAD_PAGE);
             descs[s] = make_int4(pc.b, pc.h | flags << 16, pc.rb, pc.tile);
-            if (has) {
-                const uint8_t* src = a.pg.base + page * a.pg.page_bytes +
-                                     (int64_t)((pc.h << lps) + (T0 & ((1 << lps) - 1))) * rec_bytes;
-                mbar_arrive_expect_tx(&bars[s], rec_bytes);
-                bulk_g2s(ring + (size_t)s * rec_bytes, src, rec_bytes, &bars[s]);
+            if (has && !dead) {
+                mbar_arrive_expect_tx(&bars[s], k_bytes);
+                bulk_g2s(ring + s * a.stage_bytes, src, k_bytes, &bars[s]);
             } else {
                 mbar_arrive(&bars[s]);
             }
         }
-        --left;
-        att_next<RB>(a, pc, left > 0);
+        first_of_run = false;
+        value_next = true;
     };
     int issued = 0;
     long long done = 0;
     for (; issued < a.stages && left > 0; ++issued) issue(issued);
+
+    // ---- rotated queries: rows of the CTA's items dealt out to the warps
+    float* areas = reinterpret_cast<float*>(smem + C::QAt);
+    auto query_row = [&](const AttSeq& s, int head, int rb, int r) -> const uint16_t* {
+        r += rb * RB;
+        if (r >= s.n * a.group) return nullptr;
+        const int tok = r / a.group, hq = head * a.group + (r - tok * a.group);
+        return reinterpret_cast<const uint16_t*>(a.q.p) + (s.row0 + tok) * a.q.row + hq * a.q.head;
+    };
+    if (shared_q) {
+        for (int k = 0; k < items; ++k) {
+            for (int r = warp; r < RB; r += W)
+                rotate_query<D, NT, BF16>(a, query_row(cc.s, cc.h, cc.rb, r), areas + k * C::QFloats, r >> 3, r & 7, lane);
+            cc.tile = cc.s.tiles - 1;
+            att_next<RB>(a, cc, k + 1 < items);
+        }
+        __syncthreads();
+    }
     __syncwarp();
 
     AttQ<D, NT> q;
@@ -651,6 +708,19 @@ __global__ void __launch_bounds__(32 * AttCfg<D, NT>::W, 1) kv_attend_kernel(KvA
     int qpos[NT][2], lo_pos = 0, hi_pos = 0, E2 = -14;
     bool frag_head = false;
     int stage = 0, parity = 0, in_flight = issued;
+    // the stage just read is free: fill it again and step on
+    auto next_stage = [&] {
+        __syncwarp();
+        --in_flight;
+        if (left > 0) {
+            issue(stage);
+            ++in_flight;
+        }
+        if (++stage == a.stages) {
+            stage = 0;
+            parity ^= 1;
+        }
+    };
     const int j = lane & 3, r8 = lane >> 2;
     while (in_flight > 0) {
         const int4 d = descs[stage];
@@ -658,7 +728,16 @@ __global__ void __launch_bounds__(32 * AttCfg<D, NT>::W, 1) kv_attend_kernel(KvA
         if (flags & kDescFirst) {
             cs = att_seq<RB>(a, d.x);
             const int rows = cs.n * a.group, r_base = d.z * RB;
-            load_queries<D, NT, BF16>(a, cs.row0, rows, r_base, head, lane, q);
+            const float* area = areas + (shared_q ? my_item : warp) * C::QFloats;
+            if (!shared_q) {
+                __syncwarp();
+                for (int r = 0; r < RB; ++r)
+                    rotate_query<D, NT, BF16>(a, query_row(cs, head, d.z, r), areas + warp * C::QFloats, r >> 3, r & 7,
+                                              lane);
+                __syncwarp();
+            }
+            ++my_item;
+            load_queries<D, NT>(area, lane, q);
             lo_pos = cs.pos0 + r_base / a.group;
             hi_pos = cs.pos0 + (min(r_base + RB, rows) - 1) / a.group;
 #pragma unroll
@@ -680,10 +759,10 @@ __global__ void __launch_bounds__(32 * AttCfg<D, NT>::W, 1) kv_attend_kernel(KvA
         }
         if (!mbar_wait(&bars[stage], parity)) dead = true;  // and no copy is issued any more
         dead = __any_sync(0xffffffffu, dead);
-        if (!(flags & kDescSkip) && !dead) {
-            const uint8_t* rec = ring + (size_t)stage * rec_bytes;
-            const uint8_t* vpart = rec + 4 * D * a.pg.kb + 2 * D;
-            float s[2][NT][4];
+        const bool read = !(flags & kDescSkip) && !dead;
+        float s[2][NT][4];
+        if (read) {
+            const uint8_t* rec = ring + stage * a.stage_bytes;
             switch (a.pg.kb) {
 #define QG_SCORES(B)                                                \
     case B:                                                         \
@@ -698,6 +777,12 @@ __global__ void __launch_bounds__(32 * AttCfg<D, NT>::W, 1) kv_attend_kernel(KvA
                 QG_SCORES(8)
 #undef QG_SCORES
             }
+        }
+        next_stage();
+        if (!mbar_wait(&bars[stage], parity)) dead = true;
+        dead = __any_sync(0xffffffffu, dead);
+        if (read && !dead) {
+            const uint8_t* vpart = ring + stage * a.stage_bytes;
             const int t_first = (cs.t0 + d.w) * kTileTokens;
             const bool masked = t_first + kTileTokens - 1 > lo_pos || (a.window > 0 && t_first <= hi_pos - a.window);
 #pragma unroll
@@ -742,7 +827,7 @@ __global__ void __launch_bounds__(32 * AttCfg<D, NT>::W, 1) kv_attend_kernel(KvA
                         }
                     }
             }
-            uint32_t p[2][NT][2], on[2][NT][2];
+            uint32_t p[2][NT][2];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 const float m0 = (m[nt][0] == -INFINITY ? 0.f : m[nt][0]) - kAttShift;
@@ -755,17 +840,7 @@ __global__ void __launch_bounds__(32 * AttCfg<D, NT>::W, 1) kv_attend_kernel(KvA
                     l[nt][1] += p1 + p3;
                     p[h][nt][0] = movm_trans(h2_bits(__floats2half2_rn(p0, p1)));
                     p[h][nt][1] = movm_trans(h2_bits(__floats2half2_rn(p2, p3)));
-                    on[h][nt][0] = on[h][nt][1] = 0xffffffffu;
                 }
-            }
-            if (masked) {  // a weight of 0 is 0 whatever the scale it meets
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int k = 0; k < 2; ++k)
-                            on[h][nt][k] = __hneu2_mask(bits_h2(p[h][nt][k]), bits_h2(0));
             }
             // V scales are brought below 2 by 2^-E2 of the largest seen
             __half2 es = __float2half2_rn(__uint_as_float((uint32_t)(127 - E2) << 23));
@@ -774,8 +849,8 @@ __global__ void __launch_bounds__(32 * AttCfg<D, NT>::W, 1) kv_attend_kernel(KvA
             if (__any_sync(0xffffffffu, big)) {
                 const __half2 v = v_scale_max<D>(vpart, a.pg.vb, lane, hi_pos - t_first);
                 float t = fmaxf(__low2float(v), __high2float(v));
-                t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
-                t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, o));
                 const int en = min(max((int)(__float_as_uint(t) >> 23) - 127, E2), 15);
                 const float k = __uint_as_float((uint32_t)(127 + E2 - en) << 23);
                 E2 = en;
@@ -790,8 +865,8 @@ __global__ void __launch_bounds__(32 * AttCfg<D, NT>::W, 1) kv_attend_kernel(KvA
             switch (a.pg.vb) {
 #define QG_OUTPUT(B)                                                                  \
     case B:                                                                           \
-        output_half<D, NT, B>(vpart, 0, lane, es, p[0], on[0], acc);                  \
-        output_half<D, NT, B>(vpart, 1, lane, es, p[1], on[1], acc);                  \
+        output_half<D, NT, B>(vpart, 0, lane, es, p[0], masked, acc);                 \
+        output_half<D, NT, B>(vpart, 1, lane, es, p[1], masked, acc);                 \
         break;
                 QG_OUTPUT(2)
                 QG_OUTPUT(3)
@@ -802,13 +877,8 @@ __global__ void __launch_bounds__(32 * AttCfg<D, NT>::W, 1) kv_attend_kernel(KvA
 #undef QG_OUTPUT
             }
         }
-        __syncwarp();
+        next_stage();
         ++done;
-        --in_flight;
-        if (left > 0) {
-            issue(stage);
-            ++in_flight;
-        }
         if (flags & kDescLast) {
             // this warp's part of the item is done: its slot, in the sums' own units
             // (one that began before this warp is its first, and may leave copies in flight;
@@ -913,15 +983,26 @@ __global__ void __launch_bounds__(32 * AttCfg<D, NT>::W, 1) kv_attend_kernel(KvA
                 }
             }
         }
-        if (++stage == a.stages) {
-            stage = 0;
-            parity ^= 1;
-        }
     }
     __syncthreads();
 
     // ---- join: fragments lie in order (warp, slot); those of one item are neighbours
-    int gi = 0;  // groups seen, to deal rows out to warps
+    float* weights = areas;                          // [RB][MaxCtas]
+    float* rowbuf = areas + RB * C::MaxCtas;         // [RB][D]
+    float* stats = rowbuf + RB * D;                  // [RB] maximum, [RB] sum
+    constexpr int Vecs = RB * D / 4;                 // float4s of an item's rows
+    auto slot_of = [&](int k) {
+        return (k & 1) ? reinterpret_cast<const float*>(rings + (k >> 1) * a.ring_bytes)
+                       : slots + (k >> 1) * C::SlotFloats;
+    };
+    auto store_rows = [&](const AttSeq& s, const AttFrag& fr, int rows) {
+        for (int r = warp; r < rows; r += W) {
+            float o[E];
+#pragma unroll
+            for (int i = 0; i < E; ++i) o[i] = rowbuf[r * D + E * lane + i];
+            store_row<D, BF16>(a, o, stats[r], stats[RB + r], s.row0, fr.rb * RB + r, fr.head, lane);
+        }
+    };
     for (int f = 0; f < 2 * W;) {
         const AttFrag fr = frags[f];
         if (fr.tiles == 0) {
@@ -934,38 +1015,46 @@ __global__ void __launch_bounds__(32 * AttCfg<D, NT>::W, 1) kv_attend_kernel(KvA
         const AttSeq s = att_seq<RB>(a, fr.seq);
         const int rows = min(RB, s.n * a.group - fr.rb * RB);
         float* gslot = a.partial + ((size_t)blockIdx.x * 2 + (fr.item < cta0 ? 0 : 1)) * C::GSlot;
-        for (int r = 0; r < rows; ++r) {
-            if ((gi * RB + r) % W != warp) continue;
-            float mx = -INFINITY, lt = 0.f, o[E];
-            for (int k = f; k < e; ++k) {
-                if (frags[k].tiles == 0) continue;
-                const float* sl = (k & 1) ? reinterpret_cast<const float*>(rings + (size_t)(k >> 1) * a.stages * rec_bytes)
-                                          : slots + (k >> 1) * C::SlotFloats;
-                mx = fmaxf(mx, sl[RB * C::OS + r]);
-            }
+        for (int r = warp; r < RB; r += W) {
+            const bool in = lane >= f && lane < e && frags[min(lane, 2 * W - 1)].tiles > 0;
+            const float* sl = slot_of(in ? lane : f);
+            const float ms = in ? sl[RB * C::OS + r] : -INFINITY, ls = in ? sl[RB * C::OS + RB + r] : 0.f;
+            float mx = ms;
 #pragma unroll
-            for (int i = 0; i < E; ++i) o[i] = 0.f;
-            for (int k = f; k < e; ++k) {
-                if (frags[k].tiles == 0) continue;
-                const float* sl = (k & 1) ? reinterpret_cast<const float*>(rings + (size_t)(k >> 1) * a.stages * rec_bytes)
-                                          : slots + (k >> 1) * C::SlotFloats;
-                const float ms = sl[RB * C::OS + r], w = ms == mx ? 1.f : ex2(ms - mx);
-                lt = fmaf(w, sl[RB * C::OS + RB + r], lt);
+            for (int o = 1; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            const float w = !in ? 0.f : ms == mx ? 1.f : ex2(ms - mx);
+            float lt = in ? w * ls : 0.f;
 #pragma unroll
-                for (int i = 0; i < E; ++i) o[i] = fmaf(w, sl[r * C::OS + E * lane + i], o[i]);
-            }
-            if (whole) {
-                store_row<D, BF16>(a, o, mx, lt, s.row0, fr.rb * RB + r, fr.head, lane);
-            } else {
-#pragma unroll
-                for (int i = 0; i < E; ++i) gslot[r * D + E * lane + i] = o[i];
-                if (lane == 0) {
+            for (int o = 1; o < 32; o <<= 1) lt += __shfl_xor_sync(0xffffffffu, lt, o);
+            weights[r * C::MaxCtas + lane] = w;
+            if (lane == 0) {
+                stats[r] = mx;
+                stats[RB + r] = lt;
+                if (!whole) {
                     gslot[RB * D + r] = mx;
                     gslot[RB * D + RB + r] = lt;
                 }
             }
         }
-        if (!whole) {
+        __syncthreads();
+        for (int i = threadIdx.x; i < Vecs; i += T) {
+            const int r = i / (D / 4), dd = (i % (D / 4)) * 4;
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int k = f; k < e; ++k) {
+                if (frags[k].tiles == 0) continue;
+                const float w = weights[r * C::MaxCtas + k];
+                const float4 v = *reinterpret_cast<const float4*>(slot_of(k) + r * C::OS + dd);
+                o.x = fmaf(w, v.x, o.x);
+                o.y = fmaf(w, v.y, o.y);
+                o.z = fmaf(w, v.z, o.z);
+                o.w = fmaf(w, v.w, o.w);
+            }
+            *reinterpret_cast<float4*>((whole ? rowbuf : gslot) + 4 * i) = o;
+        }
+        if (whole) {
+            __syncthreads();
+            store_rows(s, fr, rows);
+        } else {
             // the last CTA of the item to get here joins them, first to last
             const int c0 = (int)(fr.item / share), c1 = (int)((fr.item + fr.tiles - 1) / share);
             __threadfence();
@@ -978,26 +1067,52 @@ __global__ void __launch_bounds__(32 * AttCfg<D, NT>::W, 1) kv_attend_kernel(KvA
             }
             __syncthreads();
             if (sh_last) {
-                for (int r = warp; r < rows; r += W) {
-                    float mx = -INFINITY, lt = 0.f, o[E];
-                    for (int k = c0 + lane; k <= c1; k += 32)
-                        mx = fmaxf(mx, __ldcg(a.partial + ((size_t)k * 2 + (k == c0 ? 1 : 0)) * C::GSlot + RB * D + r));
+                auto part_of = [&](int k) { return a.partial + ((size_t)k * 2 + (k == c0 ? 1 : 0)) * C::GSlot; };
+                for (int r = warp; r < RB; r += W) {
+                    float ms[C::MaxCtas / 32], mx = -INFINITY, lt = 0.f;
 #pragma unroll
-                    for (int o2 = 1; o2 < 32; o2 <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o2));
-#pragma unroll
-                    for (int i = 0; i < E; ++i) o[i] = 0.f;
-                    for (int k = c0; k <= c1; ++k) {
-                        const float* sl = a.partial + ((size_t)k * 2 + (k == c0 ? 1 : 0)) * C::GSlot;
-                        const float ms = __ldcg(sl + RB * D + r), w = ms == mx ? 1.f : ex2(ms - mx);
-                        lt = fmaf(w, __ldcg(sl + RB * D + RB + r), lt);
-#pragma unroll
-                        for (int i = 0; i < E; ++i) o[i] = fmaf(w, __ldcg(sl + r * D + E * lane + i), o[i]);
+                    for (int i = 0; i < C::MaxCtas / 32; ++i) {
+                        const int k = c0 + lane + 32 * i;
+                        ms[i] = k <= c1 ? __ldcg(part_of(k) + RB * D + r) : -INFINITY;
+                        mx = fmaxf(mx, ms[i]);
                     }
-                    store_row<D, BF16>(a, o, mx, lt, s.row0, fr.rb * RB + r, fr.head, lane);
+#pragma unroll
+                    for (int o = 1; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+#pragma unroll
+                    for (int i = 0; i < C::MaxCtas / 32; ++i) {
+                        const int k = c0 + lane + 32 * i;
+                        if (k > c1) continue;
+                        const float w = ms[i] == mx ? 1.f : ex2(ms[i] - mx);
+                        lt = fmaf(w, __ldcg(part_of(k) + RB * D + RB + r), lt);
+                        weights[r * C::MaxCtas + k - c0] = w;
+                    }
+#pragma unroll
+                    for (int o = 1; o < 32; o <<= 1) lt += __shfl_xor_sync(0xffffffffu, lt, o);
+                    if (lane == 0) {
+                        stats[r] = mx;
+                        stats[RB + r] = lt;
+                    }
                 }
+                __syncthreads();
+                for (int i = threadIdx.x; i < Vecs; i += T) {
+                    const int r = i / (D / 4);
+                    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+                    for (int k = c0; k <= c1; ++k) {
+                        const float w = weights[r * C::MaxCtas + k - c0];
+                        const float4 v = __ldcg(reinterpret_cast<const float4*>(part_of(k)) + i);
+                        o.x = fmaf(w, v.x, o.x);
+                        o.y = fmaf(w, v.y, o.y);
+                        o.z = fmaf(w, v.z, o.z);
+                        o.w = fmaf(w, v.w, o.w);
+                    }
+                    *reinterpret_cast<float4*>(rowbuf + 4 * i) = o;
+                }
+                __syncthreads();
+                store_rows(s, fr, rows);
             }
         }
-        ++gi;
+        __syncthreads();
         f = e;
     }
 }

@@ -957,9 +957,12 @@ template <int D, int NT, bool BF16>
 int launch_attend(KvAttend a, DeviceInfo* dev, bool* attr, cudaStream_t s) {
     using C = AttCfg<D, NT>;
     constexpr size_t most = 226 * 1024;  // 227 KB a CTA, some of it static
-    const size_t rec = (size_t)4 * D * (a.pg.kb + a.pg.vb + 1);
-    a.stages = (int)std::min<size_t>(kAttMaxStages, (most - C::RingAt) / (C::W * rec));
-    if (a.stages < 1 || a.stages * rec < (size_t)C::SlotBytes) return QGEMM_ERR_UNSUPPORTED;
+    // a stage holds the K or the V part of a record; the ring also takes a fragment at the end
+    const size_t part = (size_t)4 * D * std::max(a.pg.kb, a.pg.vb) + 2 * D, room = (most - C::RingAt) / C::W / 128 * 128;
+    a.stages = (int)std::min<size_t>(kAttMaxStages, room / part);
+    a.stage_bytes = (int)part;
+    a.ring_bytes = (int)(std::max(a.stages * part, (size_t)C::SlotBytes) + 127) / 128 * 128;
+    if (a.stages < 1 || (size_t)a.ring_bytes > room) return QGEMM_ERR_UNSUPPORTED;
     if (!*attr) {  // a per-device setting
         if (cudaFuncSetAttribute(kv_attend_kernel<D, NT, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  (int)most) != cudaSuccess) {
@@ -968,7 +971,8 @@ int launch_attend(KvAttend a, DeviceInfo* dev, bool* attr, cudaStream_t s) {
         }
         *attr = true;
     }
-    kv_attend_kernel<D, NT, BF16><<<dev->sms, 32 * C::W, C::RingAt + C::W * a.stages * rec, s>>>(a);
+    static_assert(C::MaxCtas * 4 <= kAttendTicketBytes, "a ticket for each CTA");
+    kv_attend_kernel<D, NT, BF16><<<std::min(dev->sms, C::MaxCtas), 32 * C::W, C::RingAt + C::W * a.ring_bytes, s>>>(a);
     return launch_status();
 }
 
@@ -1366,7 +1370,7 @@ int qgemm_kv_attend(const qgemm_kv_cache* cache, const qgemm_kv_batch* batch, in
     a.scale = scale;
     DeviceInfo* dev = nullptr;
     if ((st = current_device_info(&dev)) != QGEMM_OK) return st;
-    if (ws_bytes < attend_ws_bytes(D, dev->sms) || dev->sms > (int)(kAttendTicketBytes / 4)) return QGEMM_ERR_WORKSPACE;
+    if (ws_bytes < attend_ws_bytes(D, dev->sms)) return QGEMM_ERR_WORKSPACE;
     a.group = q_heads / a.pg.heads;
     a.tickets = static_cast<unsigned int*>(d_ws);
     a.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(d_ws) + kAttendTicketBytes);
