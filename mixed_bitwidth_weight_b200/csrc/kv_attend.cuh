@@ -58,7 +58,9 @@ constexpr float kAttSlack = 4.f;     // the running maximum may be this far behi
 
 template <int D, int NT>
 struct AttCfg {
-    static constexpr int W = 8;                       // warps: 255 registers a thread, nothing spilled
+    // warps that multiply (one more feeds them): 168 registers a thread with 11, 255 with 7
+    static constexpr int W = D * NT <= 128 ? 11 : 7;
+    static constexpr int T = 32 * (W + 1);
     static constexpr int G = D / 32;
     static constexpr int RB = 8 * NT;                 // query rows of an item
     static constexpr int OS = D + 4;                  // row stride of a slot: conflict-free float4 stores
@@ -68,15 +70,18 @@ struct AttCfg {
     // an item's rotated query: [nt][g][hi, lo][lane] 16 bytes, then zq [nt][g][8], f [nt][8]
     static constexpr int QZero = NT * G * 256, QFactor = QZero + NT * G * 8;
     static constexpr int QFloats = QFactor + NT * 8, QBytes = QFloats * 4;
-    // shared memory: slots, query areas, stage descriptors, barriers, fragments, rings
+    // shared memory: slots, query areas, stage descriptors, barriers, fragments, prefix sums, rings
     static constexpr int QAt = W * SlotBytes;
-    static constexpr int DescAt = QAt + W * QBytes;
+    static constexpr int DescAt = (QAt + W * QBytes + 15) / 16 * 16;
+    static_assert(W * SlotBytes >= W * RB * D * 2, "the query rows of W items pass through the slots");
     static constexpr int BarAt = DescAt + W * 8 * 16;
-    static constexpr int FragAt = BarAt + W * 8 * 8;
-    static constexpr int RingAt = (FragAt + 2 * W * 24 + 127) / 128 * 128;
+    static constexpr int FragAt = BarAt + 2 * W * 8 * 8;  // full and empty barriers
+    static constexpr int PrefixAt = (FragAt + 2 * W * 24 + 15) / 16 * 16;
+    static constexpr int RowAt = PrefixAt;  // a row of each warp, once the prefix sums are read
+    static constexpr int RingAt = (PrefixAt + (T * 8 > 2 * D * W ? T * 8 : 2 * D * W) + 127) / 128 * 128;
     // the join's weights and row buffer lie over the query areas
     static constexpr int MaxCtas = 160;
-    static_assert(W * QBytes >= (RB * MaxCtas + RB * D + 2 * RB) * 4, "join buffers");
+    static_assert(W * QBytes >= (RB * MaxCtas + RB * D + 2 * RB * 2 * W) * 4, "join buffers");
 };
 
 // a slot's fragment: tiles [a, b) of the item whose first tile is number `item`
@@ -87,7 +92,7 @@ struct AttFrag {
 static_assert(sizeof(AttFrag) == 24 && kAttMaxStages == 8, "the shared-memory layout");
 
 QG_DEV void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -96,7 +101,7 @@ QG_DEV void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32
 // the first of a chain: starts at (c0, c1) for both row halves
 QG_DEV void mma_f16_from(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1,
                          float c0, float c1) {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%10,%11};"
         : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1));
@@ -104,9 +109,14 @@ QG_DEV void mma_f16_from(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, u
 
 QG_DEV uint32_t movm_trans(uint32_t a) {
     uint32_t d;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
     return d;
 }
+
+QG_DEV void cp_async16(void* dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+QG_DEV void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 QG_DEV float ex2(float x) {
     float y;
@@ -223,100 +233,117 @@ struct AttQ {
     float f[NT][2];  // factor of a score, log2 units
 };
 
-template <int D, int NT, int B>
-QG_DEV void scores_half(const uint8_t* rec, int half, int lane, const AttQ<D, NT>& q, float (&s)[NT][4]) {
-    constexpr int G = D / 32, NW = D * B / 64;
-    uint32_t w[NW];
-    load_words<D, B>(rec, half, lane, w);
-    // scales of tokens 16 half + r and + 8, groups in pairs
-    uint32_t sc[G];
-    {
-        const uint8_t* p = rec + 4 * D * B + (((lane >> 2) * 4 + 2 * half) * G) * 2;
-        if constexpr (G == 2) {
-            const uint2 u = *reinterpret_cast<const uint2*>(p);
-            sc[0] = u.x;
-            sc[1] = u.y;
-        } else {
-#pragma unroll
-            for (int i = 0; i < G; i += 4) {
-                const uint4 u = *reinterpret_cast<const uint4*>(p + 4 * i);
-                sc[i] = u.x;
-                sc[i + 1] = u.y;
-                sc[i + 2] = u.z;
-                sc[i + 3] = u.w;
-            }
-        }
-    }
-#pragma unroll
-    for (int g = 0; g < G; ++g) {
-        const int p0 = g * 8 * B, p1 = (G + g) * 8 * B;  // units of the two tokens
-        uint32_t a[8];
-        if constexpr (B <= 4) {
-            const uint32_t x0 = k_word<B>(w, p0), x1 = k_word<B>(w, p1);
+// A registers of one k step (0, 1) of group g: rows tokens 8 tt + r (word x0's) and 8 (tt + 1) + r (x1's)
+template <int D, int B>
+QG_DEV void k_fragment(const uint32_t (&w)[D * B / 64], int g, int step, uint32_t (&a)[4]) {
+    const int p0 = g * 8 * B, p1 = (D / 32 + g) * 8 * B;  // units of the two tokens
+    if constexpr (B <= 4) {
+        const uint32_t x0 = k_word<B>(w, p0), x1 = k_word<B>(w, p1);
+        if (step == 0) {
             a[0] = field<B, 0>(x0);
             a[1] = field<B, 0>(x1);
             a[2] = field<B, 1>(x0);
             a[3] = field<B, 1>(x1);
-            a[4] = field<B, 2 % Fld<B>::N>(x0);
-            a[5] = field<B, 2 % Fld<B>::N>(x1);
-            a[6] = field<B, 3 % Fld<B>::N>(x0);
-            a[7] = field<B, 3 % Fld<B>::N>(x1);
         } else {
+            a[0] = field<B, 2 % Fld<B>::N>(x0);
+            a[1] = field<B, 2 % Fld<B>::N>(x1);
+            a[2] = field<B, 3 % Fld<B>::N>(x0);
+            a[3] = field<B, 3 % Fld<B>::N>(x1);
+        }
+    } else {
+        const uint32_t x0 = k_word<B>(w, p0 + 4 * B * step), x1 = k_word<B>(w, p1 + 4 * B * step);
+        a[0] = field<B, 0>(x0);
+        a[1] = field<B, 0>(x1);
+        a[2] = field<B, 1>(x0);
+        a[3] = field<B, 1>(x1);
+    }
+}
+
+// Scores of a tile, s[half][nt][c].  The four dependent matrix instructions of a
+// group are issued a step at a time over all groups, so that eight chains (four
+// with 64 dims) hide each other's latency.
+template <int D, int NT, int B>
+QG_DEV void scores_tile(const uint8_t* rec, int lane, const AttQ<D, NT>& q, float (&s)[2][NT][4]) {
+    constexpr int G = D / 32, NW = D * B / 64, HB = 1;  // halves at a time
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const uint32_t x0 = k_word<B>(w, p0 + 4 * B * k), x1 = k_word<B>(w, p1 + 4 * B * k);
-                a[4 * k] = field<B, 0>(x0);
-                a[4 * k + 1] = field<B, 0>(x1);
-                a[4 * k + 2] = field<B, 1>(x0);
-                a[4 * k + 3] = field<B, 1>(x1);
+    for (int h0 = 0; h0 < 2; h0 += HB) {
+        uint32_t w[HB][NW], sc[HB][G];
+        float c[HB][NT][G][4];
+#pragma unroll
+        for (int h = 0; h < HB; ++h) {
+            load_words<D, B>(rec, h0 + h, lane, w[h]);
+            // scales of tokens 16 half + r and + 8, groups in pairs
+            const uint8_t* p = rec + 4 * D * B + (((lane >> 2) * 4 + 2 * (h0 + h)) * G) * 2;
+            if constexpr (G == 2) {
+                const uint2 u = *reinterpret_cast<const uint2*>(p);
+                sc[h][0] = u.x;
+                sc[h][1] = u.y;
+            } else {
+#pragma unroll
+                for (int i = 0; i < G; i += 4) {
+                    const uint4 u = *reinterpret_cast<const uint4*>(p + 4 * i);
+                    sc[h][i] = u.x;
+                    sc[h][i + 1] = u.y;
+                    sc[h][i + 2] = u.z;
+                    sc[h][i + 3] = u.w;
+                }
             }
         }
-        const __half2 h0 = bits_h2(sc[g / 2]), h1 = bits_h2(sc[G / 2 + g / 2]);
-        const float s0 = (g & 1) ? __high2float(h0) : __low2float(h0);
-        const float s1 = (g & 1) ? __high2float(h1) : __low2float(h1);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            float c[4];
-            mma_f16_from(c, a[0], a[1], a[2], a[3], q.hi[nt][g][0], q.hi[nt][g][1], q.zq[nt][g][0], q.zq[nt][g][1]);
-            mma_f16(c, a[4], a[5], a[6], a[7], q.hi[nt][g][2], q.hi[nt][g][3]);
-            mma_f16(c, a[0], a[1], a[2], a[3], q.lo[nt][g][0], q.lo[nt][g][1]);
-            mma_f16(c, a[4], a[5], a[6], a[7], q.lo[nt][g][2], q.lo[nt][g][3]);
+        for (int step = 0; step < 2; ++step) {
+            uint32_t a[HB][G][4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float si = i < 2 ? s0 : s1;
-                s[nt][i] = g == 0 ? c[i] * si : fmaf(c[i], si, s[nt][i]);
-            }
+            for (int h = 0; h < HB; ++h)
+#pragma unroll
+                for (int g = 0; g < G; ++g) {
+                    uint32_t(&x)[4] = a[h][g];
+                    k_fragment<D, B>(w[h], g, step, x);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        if (step == 0)
+                            mma_f16_from(c[h][nt][g], x[0], x[1], x[2], x[3], q.hi[nt][g][0], q.hi[nt][g][1],
+                                         q.zq[nt][g][0], q.zq[nt][g][1]);
+                        else
+                            mma_f16(c[h][nt][g], x[0], x[1], x[2], x[3], q.hi[nt][g][2], q.hi[nt][g][3]);
+                    }
+                }
+#pragma unroll
+            for (int h = 0; h < HB; ++h)
+#pragma unroll
+                for (int g = 0; g < G; ++g)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+                        mma_f16(c[h][nt][g], a[h][g][0], a[h][g][1], a[h][g][2], a[h][g][3], q.lo[nt][g][2 * step],
+                                q.lo[nt][g][2 * step + 1]);
         }
+#pragma unroll
+        for (int h = 0; h < HB; ++h)
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+                const __half2 u0 = bits_h2(sc[h][g / 2]), u1 = bits_h2(sc[h][G / 2 + g / 2]);
+                const float s0 = (g & 1) ? __high2float(u0) : __low2float(u0);
+                const float s1 = (g & 1) ? __high2float(u1) : __low2float(u1);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float si = i < 2 ? s0 : s1, ci = c[h][nt][g][i];
+                        s[h0 + h][nt][i] = g == 0 ? ci * si : fmaf(ci, si, s[h0 + h][nt][i]);
+                    }
+            }
     }
 }
 
 // Rotate query row n (of 8) of row tile nt, a warp to a row, split it into its two
 // parts and put them where the B operand's lanes read them (row n's dims
-// 32 g + 8 j + i are lane 4 n + j's, pair i % 4, half i / 4).  p: the row, or null.
+// 32 g + 8 j + i are lane 4 n + j's, pair i % 4, half i / 4).  p: the row in shared memory.
 template <int D, int NT, bool BF16>
 QG_DEV void rotate_query(const KvAttend& a, const uint16_t* p, float* area, int nt, int n, int lane) {
     using C = AttCfg<D, NT>;
     constexpr int E = D / 32, G = D / 32;
     float x[E];
 #pragma unroll
-    for (int i = 0; i < E; ++i) x[i] = 0.f;
-    if (p) {
-        uint16_t v[E];
-        if constexpr (E == 2) {
-            *reinterpret_cast<uint32_t*>(v) = __ldg(reinterpret_cast<const uint32_t*>(p + 2 * lane));
-        } else {
-#pragma unroll
-            for (int i = 0; i < E; i += 4) {
-                const uint2 u = __ldg(reinterpret_cast<const uint2*>(p + E * lane + i));
-                v[i] = (uint16_t)u.x;
-                v[i + 1] = (uint16_t)(u.x >> 16);
-                v[i + 2] = (uint16_t)u.y;
-                v[i + 3] = (uint16_t)(u.y >> 16);
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < E; ++i) x[i] = kv_to_float<BF16>(v[i]);
-    }
+    for (int i = 0; i < E; ++i) x[i] = kv_to_float<BF16>(p[E * lane + i]);
     fwht_warp<E>(x, lane);
     // largest magnitude into [2^14, 2^15): both fp16 parts keep their bits
     float amax = 0.f;
@@ -374,8 +401,8 @@ QG_DEV void load_queries(const float* area, int lane, AttQ<D, NT>& q) {
 // ------------------------------------------------------------------- output
 // acc += (codes of V) x (weights): half a tile.  p[nt][k]: weights of tokens
 // 16 half + 8 k + 2 j + {0, 1} for row n = lane / 4.
-template <int D, int NT, int B>
-QG_DEV void output_half(const uint8_t* part, int half, int lane, __half2 es, const uint32_t (&p)[NT][2], bool masked,
+template <int D, int NT, int B, bool Masked>
+QG_DEV void output_half(const uint8_t* part, int half, int lane, __half2 es, const uint32_t (&p)[NT][2],
                         float (&acc)[NT][D / 16][4]) {
     constexpr int G = D / 32, NW = D * B / 64, UT = D / 64 * 8 * B;  // bits of a token's units
     uint32_t w[NW];
@@ -391,7 +418,7 @@ QG_DEV void output_half(const uint8_t* part, int half, int lane, __half2 es, con
             b0[nt] = h2_bits(__hmul2(bits_h2(p[nt][0]), s0));
             b1[nt] = h2_bits(__hmul2(bits_h2(p[nt][1]), s1));
         }
-        if (masked) {  // a weight of 0 is 0 whatever the scale it meets
+        if constexpr (Masked) {  // a weight of 0 is 0 whatever the scale it meets
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 b0[nt] &= __hneu2_mask(bits_h2(p[nt][0]), bits_h2(0));
@@ -485,15 +512,14 @@ struct AttCursor {
 
 // where tile number `at` of the call lies; prefix: tiles before each thread's chunk of sequences
 template <int RB>
-QG_DEV void att_seek(const KvAttend& a, const long long* prefix, int nthreads, int chunk, long long at, int lane,
-                     AttCursor& c) {
-    int lo = 0, n = nthreads;
-    while (n > 1) {
-        const int step = (n + 31) / 32, i = lane * step;
-        const bool le = i < n && prefix[lo + i] <= at;
-        const int k = 31 - __clz(__ballot_sync(0xffffffffu, le));
-        lo += k * step;
-        n = min(step, n - k * step);
+QG_DEV void att_seek(const KvAttend& a, const long long* prefix, int nthreads, int chunk, long long at, AttCursor& c) {
+    int lo = 0, hi = min(nthreads, (a.bt.num_seqs + chunk - 1) / chunk);  // the last entry <= at is in [lo, hi)
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (prefix[mid] <= at)
+            lo = mid;
+        else
+            hi = mid;
     }
     long long rem = at - prefix[lo];
     c.b = lo * chunk;
@@ -505,7 +531,7 @@ QG_DEV void att_seek(const KvAttend& a, const long long* prefix, int nthreads, i
     }
     const long long item = div_ll(rem, c.s.tiles);
     c.tile = (int)(rem - item * c.s.tiles);
-    c.h = (int)div_ll(item, c.s.nrb);
+    c.h = (int)div_ll(item, max(c.s.nrb, 1));
     c.rb = (int)(item - (long long)c.h * c.s.nrb);
 }
 
@@ -551,24 +577,23 @@ QG_DEV void store_row(const KvAttend& a, float (&o)[D / 32], float m, float l, i
 }
 
 template <int D, int NT, bool BF16>
-__global__ void __launch_bounds__(32 * AttCfg<D, NT>::W, 1) kv_attend_kernel(KvAttend a) {
+__global__ void __launch_bounds__(AttCfg<D, NT>::T, 1) kv_attend_kernel(KvAttend a) {
     using C = AttCfg<D, NT>;
-    constexpr int W = C::W, G = C::G, RB = C::RB, E = D / 32, T = 32 * W;
+    constexpr int W = C::W, G = C::G, RB = C::RB, E = D / 32, T = C::T;
     extern __shared__ __align__(1024) uint8_t smem[];
-    __shared__ long long sh_total[33];
-    __shared__ int sh_last;
+    __shared__ long long sh_total[W + 1];
+    __shared__ int sh_last[2];
+    __shared__ int sh_dead;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int rec_bytes = kv_record_bytes<D>(a.pg.kb, a.pg.vb);
+    const int rec_bytes = kv_record_bytes<D>(a.pg.kb, a.pg.vb), k_bytes = 4 * D * a.pg.kb + 2 * D;
     float* slots = reinterpret_cast<float*>(smem);
-    int4* descs = reinterpret_cast<int4*>(smem + C::DescAt) + warp * kAttMaxStages;
-    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::BarAt) + warp * kAttMaxStages;
+    float* areas = reinterpret_cast<float*>(smem + C::QAt);
+    uint64_t* full0 = reinterpret_cast<uint64_t*>(smem + C::BarAt);
     AttFrag* frags = reinterpret_cast<AttFrag*>(smem + C::FragAt);
+    long long* prefix = reinterpret_cast<long long*>(smem + C::PrefixAt);
     uint8_t* rings = smem + C::RingAt;
-    uint8_t* ring = rings + warp * a.ring_bytes;
-    const int k_bytes = 4 * D * a.pg.kb + 2 * D, v_bytes = rec_bytes - k_bytes;
-    long long* prefix = reinterpret_cast<long long*>(smem);  // before the slots are used
 
-    // ---- the call's work, and this CTA's and warp's share
+    // ---- the call's work, this CTA's and each warp's share
     const int chunk = (a.bt.num_seqs + T - 1) / T;
     long long mine = 0;
     for (int b = threadIdx.x * chunk; b < min((int)(threadIdx.x + 1) * chunk, a.bt.num_seqs); ++b) {
@@ -582,13 +607,14 @@ __global__ void __launch_bounds__(32 * AttCfg<D, NT>::W, 1) kv_attend_kernel(KvA
         if (lane >= o) inc += v;
     }
     if (lane == 31) sh_total[warp] = inc;
-    if (lane < kAttMaxStages) mbar_init(&bars[lane], 1);
-    if (lane < 2) frags[warp * 2 + lane].tiles = 0;
+    for (int i = threadIdx.x; i < 2 * W * kAttMaxStages; i += T) mbar_init(&full0[i], 1);
+    if (threadIdx.x < 2 * W) frags[threadIdx.x].tiles = 0;
+    if (threadIdx.x == 0) sh_dead = 0;
     fence_mbar_init();
     __syncthreads();
     long long before = 0, total = 0;
 #pragma unroll
-    for (int w = 0; w < W; ++w) {
+    for (int w = 0; w <= W; ++w) {
         if (w < warp) before += sh_total[w];
         total += sh_total[w];
     }
@@ -599,387 +625,425 @@ __global__ void __launch_bounds__(32 * AttCfg<D, NT>::W, 1) kv_attend_kernel(KvA
     const long long cta0 = min(share * blockIdx.x, total), cta1 = min(cta0 + share, total);
     if (cta0 >= cta1) return;
     const long long per = (cta1 - cta0 + W - 1) / W;
-    const long long w0 = min(cta0 + per * warp, cta1), w1 = min(w0 + per, cta1);
-    AttCursor pc, cc;  // the producer's place, and the CTA's first
-    att_seek<RB>(a, prefix, T, chunk, cta0, lane, cc);
-    long long left = w1 - w0;
-    // walk the CTA's items to the warp's; where the CTA has no more than W of
-    // them, all warps share their rotated queries
-    pc = cc;
-    int my_item = 0, items = 0;
-    {
-        AttCursor c = cc;
-        long long at = cta0 - c.tile;
-        for (; items <= W && at < cta1; ++items) {
-            if (w0 >= at && w0 < at + c.s.tiles) {
-                pc = c;
-                pc.tile = (int)(w0 - at);
-                my_item = items;
-            }
-            at += c.s.tiles;
-            c.tile = c.s.tiles - 1;
-            att_next<RB>(a, c, at < cta1);
-        }
-    }
-    const bool shared_q = items <= W;
-    if (!shared_q && left > 0) att_seek<RB>(a, prefix, T, chunk, w0, lane, pc);
-    __syncthreads();  // prefix is read; slots may be written
 
-    // ---- one warp's run
-    const int lps = 31 - __clz(a.pg.page_size / kTileTokens);  // log2 tiles per page
-    int page_base = 0, page_b = -1, page_id = 0;               // lane i: page page_base + i of sequence page_b
-    int page_left = 0;                                         // tiles of the page still to come
-    bool has = false, first_of_run = true, dead = false;
-    bool value_next = false;  // copies alternate: a tile's K part, its V part
-    const uint8_t* src = nullptr;
-    auto issue = [&](int s) {
-        if (value_next) {
-            if (lane == 0) {
-                if (has && !dead) {
-                    mbar_arrive_expect_tx(&bars[s], v_bytes);
-                    bulk_g2s(ring + s * a.stage_bytes, src + k_bytes, v_bytes, &bars[s]);
-                } else {
-                    mbar_arrive(&bars[s]);
-                }
-            }
-            value_next = false;
-            src += rec_bytes;
-            --page_left;
-            --left;
-            att_next<RB>(a, pc, left > 0);
-            return;
-        }
-        if (page_left == 0 || pc.tile == 0) {
-            const int T0 = pc.s.t0 + pc.tile, pi = T0 >> lps;
-            if (page_b != pc.b || pi < page_base || pi >= page_base + 32) {
-                page_b = pc.b;
-                page_base = pi;
-                page_id = pi + lane < a.bt.max_pages && (int64_t)(pi + lane) * a.pg.page_size < pc.s.len
-                              ? a.bt.table[pc.b * a.bt.table_stride + pi + lane]
-                              : -1;
-            }
-            const int page = __shfl_sync(0xffffffffu, page_id, pi - page_base), in = T0 & ((1 << lps) - 1);
-            page_left = (1 << lps) - in;
-            has = pc.s.len > 0 && page >= 0 && page < a.pg.num_pages;
-            if (pc.s.len > 0 && !has && lane == 0) set_dev_error(QGEMM_DEV_BAD_PAGE);
-            src = a.pg.base + page * a.pg.page_bytes + (int64_t)((pc.h << lps) + in) * rec_bytes;
-        }
-        const int flags = (first_of_run || pc.tile == 0 ? kDescFirst : 0) |
-                          (left == 1 || pc.tile + 1 == pc.s.tiles ? kDescLast : 0) | (has ? 0 : kDescSkip) |
-                          (pc.tile == 0 ? kDescHead : 0) | (pc.tile + 1 == pc.s.tiles ? kDescTail : 0);
-        if (lane == 0) {
-            descs[s] = make_int4(pc.b, pc.h | flags << 16, pc.rb, pc.tile);
-            if (has && !dead) {
-                mbar_arrive_expect_tx(&bars[s], k_bytes);
-                bulk_g2s(ring + s * a.stage_bytes, src, k_bytes, &bars[s]);
-            } else {
-                mbar_arrive(&bars[s]);
-            }
-        }
-        first_of_run = false;
-        value_next = true;
-    };
-    int issued = 0;
-    long long done = 0;
-    for (; issued < a.stages && left > 0; ++issued) issue(issued);
-
-    // ---- rotated queries: rows of the CTA's items dealt out to the warps
-    float* areas = reinterpret_cast<float*>(smem + C::QAt);
-    auto query_row = [&](const AttSeq& s, int head, int rb, int r) -> const uint16_t* {
-        r += rb * RB;
-        if (r >= s.n * a.group) return nullptr;
-        const int tok = r / a.group, hq = head * a.group + (r - tok * a.group);
-        return reinterpret_cast<const uint16_t*>(a.q.p) + (s.row0 + tok) * a.q.row + hq * a.q.head;
-    };
-    if (shared_q) {
-        for (int k = 0; k < items; ++k) {
-            for (int r = warp; r < RB; r += W)
-                rotate_query<D, NT, BF16>(a, query_row(cc.s, cc.h, cc.rb, r), areas + k * C::QFloats, r >> 3, r & 7, lane);
-            cc.tile = cc.s.tiles - 1;
-            att_next<RB>(a, cc, k + 1 < items);
-        }
-        __syncthreads();
-    }
-    __syncwarp();
-
-    AttQ<D, NT> q;
-    float acc[NT][2 * G][4], m[NT][2], l[NT][2];
-    AttSeq cs{};
-    int qpos[NT][2], lo_pos = 0, hi_pos = 0, E2 = -14;
-    bool frag_head = false;
-    int stage = 0, parity = 0, in_flight = issued;
-    // the stage just read is free: fill it again and step on
-    auto next_stage = [&] {
-        __syncwarp();
-        --in_flight;
-        if (left > 0) {
-            issue(stage);
-            ++in_flight;
-        }
-        if (++stage == a.stages) {
-            stage = 0;
-            parity ^= 1;
-        }
-    };
-    const int j = lane & 3, r8 = lane >> 2;
-    while (in_flight > 0) {
-        const int4 d = descs[stage];
-        const int flags = d.y >> 16, head = d.y & 0xffff;
-        if (flags & kDescFirst) {
-            cs = att_seq<RB>(a, d.x);
-            const int rows = cs.n * a.group, r_base = d.z * RB;
-            const float* area = areas + (shared_q ? my_item : warp) * C::QFloats;
-            if (!shared_q) {
-                __syncwarp();
-                for (int r = 0; r < RB; ++r)
-                    rotate_query<D, NT, BF16>(a, query_row(cs, head, d.z, r), areas + warp * C::QFloats, r >> 3, r & 7,
-                                              lane);
-                __syncwarp();
-            }
-            ++my_item;
-            load_queries<D, NT>(area, lane, q);
-            lo_pos = cs.pos0 + r_base / a.group;
-            hi_pos = cs.pos0 + (min(r_base + RB, rows) - 1) / a.group;
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    qpos[nt][c] = cs.pos0 + (r_base + 8 * nt + 2 * j + c) / a.group;
-                    m[nt][c] = -INFINITY;
-                    l[nt][c] = 0.f;
-                }
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int i = 0; i < 2 * G; ++i)
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) acc[nt][i][c] = 0.f;
-            E2 = -14;
-            frag_head = flags & kDescHead;
-        }
-        if (!mbar_wait(&bars[stage], parity)) dead = true;  // and no copy is issued any more
-        dead = __any_sync(0xffffffffu, dead);
-        const bool read = !(flags & kDescSkip) && !dead;
-        float s[2][NT][4];
-        if (read) {
-            const uint8_t* rec = ring + stage * a.stage_bytes;
-            switch (a.pg.kb) {
-#define QG_SCORES(B)                                                \
-    case B:                                                         \
-        scores_half<D, NT, B>(rec, 0, lane, q, s[0]);               \
-        scores_half<D, NT, B>(rec, 1, lane, q, s[1]);               \
-        break;
-                QG_SCORES(2)
-                QG_SCORES(3)
-                QG_SCORES(4)
-                QG_SCORES(5)
-                QG_SCORES(6)
-                QG_SCORES(8)
-#undef QG_SCORES
-            }
-        }
-        next_stage();
-        if (!mbar_wait(&bars[stage], parity)) dead = true;
-        dead = __any_sync(0xffffffffu, dead);
-        if (read && !dead) {
-            const uint8_t* vpart = ring + stage * a.stage_bytes;
-            const int t_first = (cs.t0 + d.w) * kTileTokens;
-            const bool masked = t_first + kTileTokens - 1 > lo_pos || (a.window > 0 && t_first <= hi_pos - a.window);
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        float x = s[h][nt][c] * q.f[nt][c & 1];
-                        if (masked) {
-                            const int t = t_first + 16 * h + 8 * (c >> 1) + r8, pos = qpos[nt][c & 1];
-                            if (t > pos || (a.window > 0 && t <= pos - a.window)) x = -INFINITY;
-                        }
-                        s[h][nt][c] = x;
+    if (warp == W) {
+        // ---- the feeding warp: lane w walks warp w's run and keeps its ring full.  Copies
+        // alternate, a tile's K part and its V part; a stage is free again when its warp
+        // has arrived on the empty barrier.
+        const long long w0 = min(cta0 + per * lane, cta1);
+        long long left = lane < W ? min(w0 + per, cta1) - w0 : 0;
+        AttCursor pc;
+        if (left > 0) att_seek<RB>(a, prefix, T, chunk, w0, pc);
+        named_bar_sync(1, T);  // the prefix sums are read
+        uint64_t* full = full0 + min(lane, W - 1) * kAttMaxStages;
+        uint64_t* empty = full + W * kAttMaxStages;
+        uint8_t* ring = rings + min(lane, W - 1) * a.ring_bytes;
+        int4* descs = reinterpret_cast<int4*>(smem + C::DescAt) + min(lane, W - 1) * kAttMaxStages;
+        const int lps = 31 - __clz(a.pg.page_size / kTileTokens);  // log2 tiles per page
+        // a table entry, -1 where there is none
+        auto page_at = [&](int b, const AttSeq& s, int pi) {
+            return pi < a.bt.max_pages && ((int64_t)pi << lps) * kTileTokens < s.len
+                       ? a.bt.table[b * a.bt.table_stride + pi]
+                       : -1;
+        };
+        int stage = 0, rounds = 0, page_left = 0, next_page = 0;
+        bool value_next = false, has = false, first_of_run = true;
+        const uint8_t* src = nullptr;
+        uint32_t idle = 0;
+        uint64_t idle_since = 0;
+        while (__any_sync(0xffffffffu, left > 0)) {
+            const bool dead = *reinterpret_cast<volatile int*>(&sh_dead) != 0;
+            const bool go = left > 0 && (rounds == 0 || dead || mbar_try_wait(&empty[stage], (rounds - 1) & 1));
+            if (go) {
+                if (!value_next) {
+                    if (page_left == 0 || pc.tile == 0) {
+                        const int t = pc.s.t0 + pc.tile, pi = t >> lps, in = t & ((1 << lps) - 1);
+                        const int page = pc.tile == 0 || first_of_run ? page_at(pc.b, pc.s, pi) : next_page;
+                        next_page = page_at(pc.b, pc.s, pi + 1);  // read ahead: here when it is needed
+                        page_left = (1 << lps) - in;
+                        has = pc.s.len > 0 && page >= 0 && page < a.pg.num_pages;
+                        if (pc.s.len > 0 && !has) set_dev_error(QGEMM_DEV_BAD_PAGE);
+                        src = a.pg.base + page * a.pg.page_bytes + (int64_t)((pc.h << lps) + in) * rec_bytes;
                     }
-            // the running maximum is moved when a score has passed it by more than the slack
-            float tm[NT][2];
-            bool over = false;
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    tm[nt][c] = fmaxf(fmaxf(s[0][nt][c], s[0][nt][c + 2]), fmaxf(s[1][nt][c], s[1][nt][c + 2]));
-                    over |= tm[nt][c] > m[nt][c] + kAttSlack;
+                    const bool last = pc.tile + 1 == pc.s.tiles;
+                    const int flags = (first_of_run || pc.tile == 0 ? kDescFirst : 0) |
+                                      (left == 1 || last ? kDescLast : 0) | (has ? 0 : kDescSkip) |
+                                      (pc.tile == 0 ? kDescHead : 0) | (last ? kDescTail : 0);
+                    first_of_run = false;
+                    descs[stage] = make_int4(pc.b, pc.h | flags << 16, pc.rb, pc.tile);
                 }
-            if (__any_sync(0xffffffffu, over)) {
+                const int bytes = value_next ? rec_bytes - k_bytes : k_bytes;
+                if (has && !dead) {
+                    mbar_arrive_expect_tx(&full[stage], bytes);
+                    bulk_g2s(ring + stage * a.stage_bytes, src, bytes, &full[stage]);
+                } else {
+                    mbar_arrive(&full[stage]);
+                }
+                src += bytes;
+                if (value_next) {
+                    --page_left;
+                    --left;
+                    att_next<RB>(a, pc, left > 0);
+                }
+                value_next = !value_next;
+                if (++stage == a.stages) {
+                    stage = 0;
+                    ++rounds;
+                }
+            }
+            if (__any_sync(0xffffffffu, go)) {
+                idle = 0;
+            } else if ((++idle & 1023u) == 0) {  // a bounded wait: the warps' own waits give up after a second
+                const uint64_t now = globaltimer_ns();
+                if (idle == 1024) idle_since = now;
+                if (__any_sync(0xffffffffu, now - idle_since > 2000000000ull)) break;
+            }
+        }
+        if (*reinterpret_cast<volatile int*>(&sh_dead) != 0 && lane < W) {
+            // copies still in flight: each stage's last one
+            for (int s = 0; s < a.stages; ++s) {
+                const int r = s < stage ? rounds : rounds - 1;
+                if (r >= 0) mbar_wait(&full[s], r & 1);
+            }
+        }
+        __syncwarp();
+    } else {
+        const long long w0 = min(cta0 + per * warp, cta1);
+        const int count = (int)(min(w0 + per, cta1) - w0);
+        // Where the CTA has no more than W items all warps share their rotated queries: each
+        // warp fetches and rotates some of the rows.
+        uint16_t* raw = reinterpret_cast<uint16_t*>(smem);  // [item][RB][D], over the slots
+        auto fetch_row = [&](const AttSeq& s, int head, int rb, int r, uint16_t* dst) {
+            r += rb * RB;
+            const uint16_t* p = nullptr;
+            if (r < s.n * a.group) {
+                const int tok = r / a.group, hq = head * a.group + (r - tok * a.group);
+                p = reinterpret_cast<const uint16_t*>(a.q.p) + (s.row0 + tok) * a.q.row + hq * a.q.head;
+            }
+            for (int i = lane * 8; i < D; i += 256) {  // 16 bytes a lane
+                if (p)
+                    cp_async16(dst + i, p + i);
+                else
+                    *reinterpret_cast<uint4*>(dst + i) = make_uint4(0, 0, 0, 0);
+            }
+        };
+        int my_item = 0, items = 0;
+        {
+            AttCursor c;
+            att_seek<RB>(a, prefix, T, chunk, cta0, c);
+            long long at = cta0 - c.tile;
+            for (; items <= W && at < cta1; ++items) {
+                if (items < W)
+                    for (int r = (warp + W - items % W * RB % W) % W; r < RB; r += W)
+                        fetch_row(c.s, c.h, c.rb, r, raw + (items * RB + r) * D);
+                if (w0 >= at && w0 < at + c.s.tiles) my_item = items;
+                at += c.s.tiles;
+                c.tile = c.s.tiles - 1;
+                att_next<RB>(a, c, at < cta1);
+            }
+        }
+        const bool shared_q = items <= W;
+        cp_async_wait_all();
+        __syncwarp();
+        if (shared_q)
+            for (int i = 0; i < items; ++i)
+                for (int r = (warp + W - i % W * RB % W) % W; r < RB; r += W)
+                    rotate_query<D, NT, BF16>(a, raw + (i * RB + r) * D, areas + i * C::QFloats, r >> 3, r & 7, lane);
+        named_bar_sync(1, T);
+
+        // ---- one warp's run
+        uint64_t* full = full0 + warp * kAttMaxStages;
+        uint64_t* empty = full + W * kAttMaxStages;
+        const uint8_t* ring = rings + warp * a.ring_bytes;
+        const int4* descs = reinterpret_cast<const int4*>(smem + C::DescAt) + warp * kAttMaxStages;
+        AttQ<D, NT> q;
+        float acc[NT][2 * G][4], m[NT][2], mo[NT][2], l[NT][2];
+        AttSeq cs{};
+        int qpos[NT][2], lo_pos = 0, hi_pos = 0, E2 = -14;
+        bool frag_head = false, dead = false;
+        int stage = 0, parity = 0;
+        const int j = lane & 3, r8 = lane >> 2;
+        auto arrived = [&] {
+            if (!dead && !__all_sync(0xffffffffu, mbar_wait(&full[stage], parity))) {
+                dead = true;  // the feeding warp stops copying
+                if (lane == 0) *reinterpret_cast<volatile int*>(&sh_dead) = 1;
+            }
+        };
+        auto release = [&] {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&empty[stage]);
+            if (++stage == a.stages) {
+                stage = 0;
+                parity ^= 1;
+            }
+        };
+        for (int done = 0; done < count; ++done) {
+            arrived();
+            const int4 d = descs[stage];
+            const int flags = d.y >> 16, head = d.y & 0xffff;
+            if (flags & kDescFirst) {
+                cs = att_seq<RB>(a, d.x);
+                const int rows = cs.n * a.group, r_base = d.z * RB;
+                if (!shared_q) {
+                    uint16_t* row = reinterpret_cast<uint16_t*>(smem + C::RowAt) + warp * D;
+                    for (int r = 0; r < RB; ++r) {
+                        __syncwarp();
+                        fetch_row(cs, head, d.z, r, row);
+                        cp_async_wait_all();
+                        __syncwarp();
+                        rotate_query<D, NT, BF16>(a, row, areas + warp * C::QFloats, r >> 3, r & 7, lane);
+                    }
+                    __syncwarp();
+                }
+                load_queries<D, NT>(areas + (shared_q ? my_item : warp) * C::QFloats, lane, q);
+                ++my_item;
+                lo_pos = cs.pos0 + r_base / a.group;
+                hi_pos = cs.pos0 + (min(r_base + RB, rows) - 1) / a.group;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
-                        float t = tm[nt][c];
-#pragma unroll
-                        for (int o = 4; o < 32; o <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, o));
-                        const float mn = fmaxf(m[nt][c], t);
-                        const float k = m[nt][c] == mn ? 1.f : ex2(m[nt][c] - mn);
-                        m[nt][c] = mn;
-                        l[nt][c] *= k;
-#pragma unroll
-                        for (int i = 0; i < 2 * G; ++i) {
-                            acc[nt][i][c] *= k;
-                            acc[nt][i][c + 2] *= k;
-                        }
+                        qpos[nt][c] = cs.pos0 + (r_base + 8 * nt + 2 * j + c) / a.group;
+                        m[nt][c] = -INFINITY;
+                        mo[nt][c] = -kAttShift;
+                        l[nt][c] = 0.f;
                     }
-            }
-            uint32_t p[2][NT][2];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                const float m0 = (m[nt][0] == -INFINITY ? 0.f : m[nt][0]) - kAttShift;
-                const float m1 = (m[nt][1] == -INFINITY ? 0.f : m[nt][1]) - kAttShift;
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const float p0 = ex2(s[h][nt][0] - m0), p1 = ex2(s[h][nt][1] - m1);
-                    const float p2 = ex2(s[h][nt][2] - m0), p3 = ex2(s[h][nt][3] - m1);
-                    l[nt][0] += p0 + p2;
-                    l[nt][1] += p1 + p3;
-                    p[h][nt][0] = movm_trans(h2_bits(__floats2half2_rn(p0, p1)));
-                    p[h][nt][1] = movm_trans(h2_bits(__floats2half2_rn(p2, p3)));
-                }
-            }
-            // V scales are brought below 2 by 2^-E2 of the largest seen
-            __half2 es = __float2half2_rn(__uint_as_float((uint32_t)(127 - E2) << 23));
-            const __half2 vm = __hmul2(v_scale_max<D>(vpart, a.pg.vb, lane, hi_pos - t_first), es);
-            const bool big = __low2float(vm) >= 2.f || __high2float(vm) >= 2.f;
-            if (__any_sync(0xffffffffu, big)) {
-                const __half2 v = v_scale_max<D>(vpart, a.pg.vb, lane, hi_pos - t_first);
-                float t = fmaxf(__low2float(v), __high2float(v));
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, o));
-                const int en = min(max((int)(__float_as_uint(t) >> 23) - 127, E2), 15);
-                const float k = __uint_as_float((uint32_t)(127 + E2 - en) << 23);
-                E2 = en;
-                es = __float2half2_rn(__uint_as_float((uint32_t)(127 - E2) << 23));
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int i = 0; i < 2 * G; ++i)
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) acc[nt][i][c] *= k;
+                        for (int c = 0; c < 4; ++c) acc[nt][i][c] = 0.f;
+                E2 = -14;
+                frag_head = flags & kDescHead;
             }
-            switch (a.pg.vb) {
-#define QG_OUTPUT(B)                                                                  \
-    case B:                                                                           \
-        output_half<D, NT, B>(vpart, 0, lane, es, p[0], masked, acc);                 \
-        output_half<D, NT, B>(vpart, 1, lane, es, p[1], masked, acc);                 \
+            const bool skip = (flags & kDescSkip) || dead;
+            float s[2][NT][4];
+            if (!skip) {
+                const uint8_t* rec = ring + stage * a.stage_bytes;
+                switch (a.pg.kb) {
+#define QG_SCORES(B)                            \
+    case B:                                     \
+        scores_tile<D, NT, B>(rec, lane, q, s); \
         break;
-                QG_OUTPUT(2)
-                QG_OUTPUT(3)
-                QG_OUTPUT(4)
-                QG_OUTPUT(5)
-                QG_OUTPUT(6)
-                QG_OUTPUT(8)
-#undef QG_OUTPUT
-            }
-        }
-        next_stage();
-        ++done;
-        if (flags & kDescLast) {
-            // this warp's part of the item is done: its slot, in the sums' own units
-            // (one that began before this warp is its first, and may leave copies in flight;
-            // one that goes on behind it is its last, and finds the ring drained)
-            float* slot = frag_head ? reinterpret_cast<float*>(ring) : slots + warp * C::SlotFloats;
-            AttFrag& fr = frags[warp * 2 + (frag_head ? 1 : 0)];
-            float unit[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                unit[i] = __uint_as_float((uint32_t)(127 + 24 + E2 - field_at(a.pg.vb, i)) << 23);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-#pragma unroll
-                    for (int o = 4; o < 32; o <<= 1) l[nt][c] += __shfl_xor_sync(0xffffffffu, l[nt][c], o);
+                    QG_SCORES(2)
+                    QG_SCORES(3)
+                    QG_SCORES(4)
+                    QG_SCORES(5)
+                    QG_SCORES(6)
+                    QG_SCORES(8)
+#undef QG_SCORES
                 }
-            if (frag_head && (flags & kDescTail)) {
-                // the whole item: rotate back in this layout (dim 32 g + 4 r + i) and store
+            }
+            release();
+            arrived();
+            if (!skip && !dead) {
+                const uint8_t* vpart = ring + stage * a.stage_bytes;
+                const int t_first = (cs.t0 + d.w) * kTileTokens;
+                const bool masked = t_first + kTileTokens - 1 > lo_pos || (a.window > 0 && t_first <= hi_pos - a.window);
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) s[h][nt][c] *= q.f[nt][c & 1];
+                if (masked) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int c = 0; c < 4; ++c) {
+                                const int t = t_first + 16 * h + 8 * (c >> 1) + r8, pos = qpos[nt][c & 1];
+                                if (t > pos || (a.window > 0 && t <= pos - a.window)) s[h][nt][c] = -INFINITY;
+                            }
+                }
+                // The running maximum is moved when a score has passed it by more than the
+                // slack, the V scales' exponent when one has reached 2 with it.
+                float tm[NT][2];
+                bool over = false;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
-                        float x[G][4];
+                        tm[nt][c] = fmaxf(fmaxf(s[0][nt][c], s[0][nt][c + 2]), fmaxf(s[1][nt][c], s[1][nt][c + 2]));
+                        over |= tm[nt][c] > m[nt][c] + kAttSlack;
+                    }
+                const __half2 vmax = v_scale_max<D>(vpart, a.pg.vb, lane, hi_pos - t_first);
+                const float vm = fmaxf(__low2float(vmax), __high2float(vmax));
+                const bool big = vm >= __uint_as_float((uint32_t)(128 + E2) << 23);
+                if (__any_sync(0xffffffffu, over || big)) {
 #pragma unroll
-                        for (int g = 0; g < G; ++g)
+                    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) x[g][i] = acc[nt][2 * g + (i >> 1)][(i & 1) * 2 + c] * unit[i];
+                        for (int c = 0; c < 2; ++c) {
+                            float t = tm[nt][c];
 #pragma unroll
-                        for (int g = 0; g < G; ++g) {
+                            for (int o = 4; o < 32; o <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, o));
+                            const float mn = fmaxf(m[nt][c], t);
+                            const float k = m[nt][c] == mn ? 1.f : ex2(m[nt][c] - mn);
+                            m[nt][c] = mn;
+                            mo[nt][c] = (mn == -INFINITY ? 0.f : mn) - kAttShift;
+                            l[nt][c] *= k;
 #pragma unroll
-                            for (int st = 1; st < 4; st <<= 1)
-#pragma unroll
-                                for (int i = 0; i < 4; ++i)
-                                    if (!(i & st)) {
-                                        const float u = x[g][i], v = x[g][i + st];
-                                        x[g][i] = u + v;
-                                        x[g][i + st] = u - v;
-                                    }
-#pragma unroll
-                            for (int ls = 4; ls < 32; ls <<= 1)
-#pragma unroll
-                                for (int i = 0; i < 4; ++i) {
-                                    const float o = __shfl_xor_sync(0xffffffffu, x[g][i], ls);
-                                    x[g][i] = (lane & ls) ? o - x[g][i] : x[g][i] + o;
-                                }
+                            for (int i = 0; i < 2 * G; ++i) {
+                                acc[nt][i][c] *= k;
+                                acc[nt][i][c + 2] *= k;
+                            }
                         }
+                    if (__any_sync(0xffffffffu, big)) {
+                        float t = vm;
 #pragma unroll
-                        for (int st = 1; st < G; st <<= 1)
+                        for (int o = 1; o < 32; o <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, o));
+                        const int en = min(max((int)(__float_as_uint(t) >> 23) - 127, E2), 15);
+                        const float k = __uint_as_float((uint32_t)(127 + E2 - en) << 23);
+                        E2 = en;
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int i = 0; i < 2 * G; ++i)
+#pragma unroll
+                                for (int c = 0; c < 4; ++c) acc[nt][i][c] *= k;
+                    }
+                }
+                uint32_t p[2][NT][2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        const float p0 = ex2(s[h][nt][0] - mo[nt][0]), p1 = ex2(s[h][nt][1] - mo[nt][1]);
+                        const float p2 = ex2(s[h][nt][2] - mo[nt][0]), p3 = ex2(s[h][nt][3] - mo[nt][1]);
+                        l[nt][0] += p0 + p2;
+                        l[nt][1] += p1 + p3;
+                        p[h][nt][0] = movm_trans(h2_bits(__floats2half2_rn(p0, p1)));
+                        p[h][nt][1] = movm_trans(h2_bits(__floats2half2_rn(p2, p3)));
+                    }
+                const __half2 es = __half2half2(__ushort_as_half((uint16_t)((15 - E2) << 10)));  // 2^-E2
+                // (15 - E2 is 0 for E2 = 15: the subnormal 2^-15)
+                const __half2 down = E2 == 15 ? bits_h2(0x02000200u) : es;
+                switch (a.pg.vb) {
+#define QG_OUTPUT(B)                                                   \
+    case B:                                                            \
+        if (masked) {                                                  \
+            output_half<D, NT, B, true>(vpart, 0, lane, down, p[0], acc);  \
+            output_half<D, NT, B, true>(vpart, 1, lane, down, p[1], acc);  \
+        } else {                                                       \
+            output_half<D, NT, B, false>(vpart, 0, lane, down, p[0], acc); \
+            output_half<D, NT, B, false>(vpart, 1, lane, down, p[1], acc); \
+        }                                                              \
+        break;
+                    QG_OUTPUT(2)
+                    QG_OUTPUT(3)
+                    QG_OUTPUT(4)
+                    QG_OUTPUT(5)
+                    QG_OUTPUT(6)
+                    QG_OUTPUT(8)
+#undef QG_OUTPUT
+                }
+            }
+            release();
+            if (flags & kDescLast) {
+                // this warp's part of the item is done: its slot, in the sums' own units
+                // (one that began before this warp is its first, and may leave copies in flight;
+                // one that goes on behind it is its last, and finds the ring drained)
+                float* slot = frag_head ? reinterpret_cast<float*>(rings + warp * a.ring_bytes) : slots + warp * C::SlotFloats;
+                AttFrag& fr = frags[warp * 2 + (frag_head ? 1 : 0)];
+                float unit[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    unit[i] = __uint_as_float((uint32_t)(127 + 24 + E2 - field_at(a.pg.vb, i)) << 23);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+#pragma unroll
+                        for (int o = 4; o < 32; o <<= 1) l[nt][c] += __shfl_xor_sync(0xffffffffu, l[nt][c], o);
+                    }
+                if (frag_head && (flags & kDescTail)) {
+                    // the whole item: rotate back in this layout (dim 32 g + 4 r + i) and store
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            float x[G][4];
 #pragma unroll
                             for (int g = 0; g < G; ++g)
-                                if (!(g & st))
 #pragma unroll
-                                    for (int i = 0; i < 4; ++i) {
-                                        const float u = x[g][i], v = x[g + st][i];
-                                        x[g][i] = u + v;
-                                        x[g + st][i] = u - v;
-                                    }
-                        const int r = d.z * RB + 8 * nt + 2 * j + c;
-                        if (r < cs.n * a.group) {
-                            const int tok = r / a.group, hq = head * a.group + (r - tok * a.group);
-                            const float inv = l[nt][c] == 0.f ? 0.f : 1.f / (l[nt][c] * (float)D);
-                            uint16_t* o = reinterpret_cast<uint16_t*>(a.out.p) + (cs.row0 + tok) * a.out.row +
-                                          hq * a.out.head + 4 * r8;
+                                for (int i = 0; i < 4; ++i) x[g][i] = acc[nt][2 * g + (i >> 1)][(i & 1) * 2 + c] * unit[i];
 #pragma unroll
                             for (int g = 0; g < G; ++g) {
-                                uint16_t v[4];
 #pragma unroll
-                                for (int i = 0; i < 4; ++i) v[i] = kv_from_float<BF16>(x[g][i] * inv);
-                                *reinterpret_cast<uint2*>(o + 32 * g) =
-                                    make_uint2(v[0] | (uint32_t)v[1] << 16, v[2] | (uint32_t)v[3] << 16);
+                                for (int st = 1; st < 4; st <<= 1)
+#pragma unroll
+                                    for (int i = 0; i < 4; ++i)
+                                        if (!(i & st)) {
+                                            const float u = x[g][i], v = x[g][i + st];
+                                            x[g][i] = u + v;
+                                            x[g][i + st] = u - v;
+                                        }
+#pragma unroll
+                                for (int ls = 4; ls < 32; ls <<= 1)
+#pragma unroll
+                                    for (int i = 0; i < 4; ++i) {
+                                        const float o = __shfl_xor_sync(0xffffffffu, x[g][i], ls);
+                                        x[g][i] = (lane & ls) ? o - x[g][i] : x[g][i] + o;
+                                    }
                             }
-                            if (a.lse && r8 == 0)
-                                a.lse[(int64_t)(cs.row0 + tok) * a.q_heads + hq] =
-                                    (m[nt][c] + log2f(l[nt][c]) - kAttShift) * 0.6931471805599453f;
+#pragma unroll
+                            for (int st = 1; st < G; st <<= 1)
+#pragma unroll
+                                for (int g = 0; g < G; ++g)
+                                    if (!(g & st))
+#pragma unroll
+                                        for (int i = 0; i < 4; ++i) {
+                                            const float u = x[g][i], v = x[g + st][i];
+                                            x[g][i] = u + v;
+                                            x[g + st][i] = u - v;
+                                        }
+                            const int r = d.z * RB + 8 * nt + 2 * j + c;
+                            if (r < cs.n * a.group) {
+                                const int tok = r / a.group, hq = head * a.group + (r - tok * a.group);
+                                const float inv = l[nt][c] == 0.f ? 0.f : 1.f / (l[nt][c] * (float)D);
+                                uint16_t* o = reinterpret_cast<uint16_t*>(a.out.p) + (cs.row0 + tok) * a.out.row +
+                                              hq * a.out.head + 4 * r8;
+#pragma unroll
+                                for (int g = 0; g < G; ++g) {
+                                    uint16_t v[4];
+#pragma unroll
+                                    for (int i = 0; i < 4; ++i) v[i] = kv_from_float<BF16>(x[g][i] * inv);
+                                    *reinterpret_cast<uint2*>(o + 32 * g) =
+                                        make_uint2(v[0] | (uint32_t)v[1] << 16, v[2] | (uint32_t)v[3] << 16);
+                                }
+                                if (a.lse && r8 == 0)
+                                    a.lse[(int64_t)(cs.row0 + tok) * a.q_heads + hq] =
+                                        (m[nt][c] + log2f(l[nt][c]) - kAttShift) * 0.6931471805599453f;
+                            }
                         }
-                    }
-            } else {
-                __syncwarp();
+                } else {
+                    __syncwarp();
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+                    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        const int r = 8 * nt + 2 * j + c;
+                        for (int c = 0; c < 2; ++c) {
+                            const int r = 8 * nt + 2 * j + c;
 #pragma unroll
-                        for (int g = 0; g < G; ++g)
-                            *reinterpret_cast<float4*>(slot + r * C::OS + 32 * g + 4 * r8) =
-                                make_float4(acc[nt][2 * g][c] * unit[0], acc[nt][2 * g][c + 2] * unit[1],
-                                            acc[nt][2 * g + 1][c] * unit[2], acc[nt][2 * g + 1][c + 2] * unit[3]);
-                        if (r8 == 0) {
-                            slot[RB * C::OS + r] = m[nt][c];
-                            slot[RB * C::OS + RB + r] = l[nt][c];
+                            for (int g = 0; g < G; ++g)
+                                *reinterpret_cast<float4*>(slot + r * C::OS + 32 * g + 4 * r8) =
+                                    make_float4(acc[nt][2 * g][c] * unit[0], acc[nt][2 * g][c + 2] * unit[1],
+                                                acc[nt][2 * g + 1][c] * unit[2], acc[nt][2 * g + 1][c + 2] * unit[3]);
+                            if (r8 == 0) {
+                                slot[RB * C::OS + r] = m[nt][c];
+                                slot[RB * C::OS + RB + r] = l[nt][c];
+                            }
                         }
+                    if (lane == 0) {
+                        // the item's first tile as a number of the call: this tile's less its place
+                        fr.item = w0 + done - d.w;
+                        fr.seq = d.x;
+                        fr.head = head;
+                        fr.rb = d.z;
+                        fr.tiles = cs.tiles;
                     }
-                if (lane == 0) {
-                    // the item's first tile as a number of the call: this tile's less its place
-                    fr.item = w0 + done - 1 - d.w;
-                    fr.seq = d.x;
-                    fr.head = head;
-                    fr.rb = d.z;
-                    fr.tiles = cs.tiles;
                 }
             }
         }
@@ -989,131 +1053,154 @@ __global__ void __launch_bounds__(32 * AttCfg<D, NT>::W, 1) kv_attend_kernel(KvA
     // ---- join: fragments lie in order (warp, slot); those of one item are neighbours
     float* weights = areas;                          // [RB][MaxCtas]
     float* rowbuf = areas + RB * C::MaxCtas;         // [RB][D]
-    float* stats = rowbuf + RB * D;                  // [RB] maximum, [RB] sum
+    float* stats = rowbuf + RB * D;                  // [RB][2 W] maxima, then sums, by the group's first fragment
     constexpr int Vecs = RB * D / 4;                 // float4s of an item's rows
     auto slot_of = [&](int k) {
-        return (k & 1) ? reinterpret_cast<const float*>(rings + (k >> 1) * a.ring_bytes)
-                       : slots + (k >> 1) * C::SlotFloats;
+        return (k & 1) ? reinterpret_cast<float*>(rings + (k >> 1) * a.ring_bytes) : slots + (k >> 1) * C::SlotFloats;
     };
-    auto store_rows = [&](const AttSeq& s, const AttFrag& fr, int rows) {
-        for (int r = warp; r < rows; r += W) {
-            float o[E];
+    // lane k < 2 W: fragment k, the first and the last of its group
+    const AttFrag fr = frags[min(lane, 2 * W - 1)];
+    const bool active = lane < 2 * W && fr.tiles > 0;
+    const uint32_t act = __ballot_sync(0xffffffffu, active);
+    if (act == 0) return;
+    const uint32_t below = act & ((1u << lane) - 1u);
+    const int prev = below ? 31 - __clz(below) : 0;
+    const long long prev_item = __shfl_sync(0xffffffffu, fr.item, prev);
+    const uint32_t heads = __ballot_sync(0xffffffffu, active && (below == 0 || prev_item != fr.item));
+    const uint32_t upto = heads & ((2u << lane) - 1u), above = heads & ~((2u << lane) - 1u);
+    const int gfirst = upto ? 31 - __clz(upto) : 0, gend = above ? __ffs(above) - 1 : 2 * W;
+    const bool whole = fr.item >= cta0 && fr.item + fr.tiles <= cta1;
+    for (int r = warp; r < RB; r += W + 1) {
+        const float* sl = slot_of(active ? lane : gfirst);
+        const float ms = active ? sl[RB * C::OS + r] : -INFINITY, ls = active ? sl[RB * C::OS + RB + r] : 0.f;
+        float mx = ms;
 #pragma unroll
-            for (int i = 0; i < E; ++i) o[i] = rowbuf[r * D + E * lane + i];
-            store_row<D, BF16>(a, o, stats[r], stats[RB + r], s.row0, fr.rb * RB + r, fr.head, lane);
+        for (int o = 1; o < 2 * W; o <<= 1) {
+            const float v = __shfl_up_sync(0xffffffffu, mx, o);
+            if (lane - o >= gfirst) mx = fmaxf(mx, v);
         }
-    };
-    for (int f = 0; f < 2 * W;) {
-        const AttFrag fr = frags[f];
-        if (fr.tiles == 0) {
-            ++f;
-            continue;
+        mx = __shfl_sync(0xffffffffu, mx, gend - 1);
+        const float w = !active ? 0.f : ms == mx ? 1.f : ex2(ms - mx);
+        float lt = active ? w * ls : 0.f;
+#pragma unroll
+        for (int o = 1; o < 2 * W; o <<= 1) {
+            const float v = __shfl_up_sync(0xffffffffu, lt, o);
+            if (lane - o >= gfirst) lt += v;
         }
-        int e = f + 1;
-        while (e < 2 * W && (frags[e].tiles == 0 || frags[e].item == fr.item)) ++e;
-        const bool whole = fr.item >= cta0 && fr.item + fr.tiles <= cta1;
-        const AttSeq s = att_seq<RB>(a, fr.seq);
-        const int rows = min(RB, s.n * a.group - fr.rb * RB);
-        float* gslot = a.partial + ((size_t)blockIdx.x * 2 + (fr.item < cta0 ? 0 : 1)) * C::GSlot;
-        for (int r = warp; r < RB; r += W) {
-            const bool in = lane >= f && lane < e && frags[min(lane, 2 * W - 1)].tiles > 0;
-            const float* sl = slot_of(in ? lane : f);
-            const float ms = in ? sl[RB * C::OS + r] : -INFINITY, ls = in ? sl[RB * C::OS + RB + r] : 0.f;
-            float mx = ms;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-            const float w = !in ? 0.f : ms == mx ? 1.f : ex2(ms - mx);
-            float lt = in ? w * ls : 0.f;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) lt += __shfl_xor_sync(0xffffffffu, lt, o);
-            weights[r * C::MaxCtas + lane] = w;
-            if (lane == 0) {
-                stats[r] = mx;
-                stats[RB + r] = lt;
-                if (!whole) {
-                    gslot[RB * D + r] = mx;
-                    gslot[RB * D + RB + r] = lt;
-                }
+        if (lane < 2 * W) weights[r * C::MaxCtas + lane] = w;
+        lt = __shfl_sync(0xffffffffu, lt, gend - 1);
+        if (heads >> lane & 1) {
+            stats[r * 2 * W + lane] = mx;
+            stats[(RB + r) * 2 * W + lane] = lt;
+            if (!whole) {
+                float* gslot = a.partial + ((size_t)blockIdx.x * 2 + (fr.item < cta0 ? 0 : 1)) * C::GSlot;
+                gslot[RB * D + r] = mx;
+                gslot[RB * D + RB + r] = lt;
             }
         }
-        __syncthreads();
+    }
+    __syncthreads();
+    // each group's sum of weighted fragments into its first one (element by element the same thread's), or out
+    const uint32_t wholes = __ballot_sync(0xffffffffu, whole) & heads;
+    for (uint32_t hs = heads; hs; hs &= hs - 1) {
+        const int f = __ffs(hs) - 1, e = __shfl_sync(0xffffffffu, gend, f);
+        const long long item = __shfl_sync(0xffffffffu, fr.item, f);
+        float* dst = a.partial + ((size_t)blockIdx.x * 2 + (item < cta0 ? 0 : 1)) * C::GSlot;
         for (int i = threadIdx.x; i < Vecs; i += T) {
-            const int r = i / (D / 4), dd = (i % (D / 4)) * 4;
+            const int r = i / (D / 4), at = r * C::OS + (i % (D / 4)) * 4;
             float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int k = f; k < e; ++k) {
-                if (frags[k].tiles == 0) continue;
+            for (uint32_t ks = act & ~((1u << f) - 1u) & (uint32_t)((1ull << e) - 1u); ks; ks &= ks - 1) {
+                const int k = __ffs(ks) - 1;
                 const float w = weights[r * C::MaxCtas + k];
-                const float4 v = *reinterpret_cast<const float4*>(slot_of(k) + r * C::OS + dd);
+                const float4 v = *reinterpret_cast<const float4*>(slot_of(k) + at);
                 o.x = fmaf(w, v.x, o.x);
                 o.y = fmaf(w, v.y, o.y);
                 o.z = fmaf(w, v.z, o.z);
                 o.w = fmaf(w, v.w, o.w);
             }
-            *reinterpret_cast<float4*>((whole ? rowbuf : gslot) + 4 * i) = o;
+            if (wholes >> f & 1)
+                *reinterpret_cast<float4*>(slot_of(f) + at) = o;
+            else
+                *reinterpret_cast<float4*>(dst + 4 * i) = o;
         }
-        if (whole) {
-            __syncthreads();
-            store_rows(s, fr, rows);
-        } else {
-            // the last CTA of the item to get here joins them, first to last
-            const int c0 = (int)(fr.item / share), c1 = (int)((fr.item + fr.tiles - 1) / share);
-            __threadfence();
-            __syncthreads();
-            if (threadIdx.x == 0) {
-                const bool last = atomicAdd(&a.tickets[c0], 1u) == (unsigned)(c1 - c0);
-                if (last) a.tickets[c0] = 0;
-                __threadfence();
-                sh_last = last;
+    }
+    if (wholes != heads) __threadfence();
+    __syncthreads();
+    // a group that goes on in other CTAs: its last CTA to get here joins them (at most two
+    // groups a CTA; the ticket is that of the item's first CTA)
+    if (warp == 0 && (heads >> lane & 1) && !whole) {
+        const int c0 = (int)(fr.item / share), c1 = (int)((fr.item + fr.tiles - 1) / share);
+        const bool last = atomicAdd(&a.tickets[c0], 1u) == (unsigned)(c1 - c0);
+        if (last) a.tickets[c0] = 0;
+        __threadfence();
+        sh_last[fr.item < cta0 ? 0 : 1] = last;
+    }
+    for (int i = warp; i < __popc(wholes) * RB; i += W + 1) {
+        const int f = __fns(wholes, 0, i / RB + 1), r = i % RB;
+        const AttFrag& g = frags[f];
+        const AttSeq s = att_seq<RB>(a, g.seq);
+        if (g.rb * RB + r >= s.n * a.group) continue;
+        float o[E];
+#pragma unroll
+        for (int k = 0; k < E; ++k) o[k] = slot_of(f)[r * C::OS + E * lane + k];
+        store_row<D, BF16>(a, o, stats[r * 2 * W + f], stats[(RB + r) * 2 * W + f], s.row0, g.rb * RB + r, g.head, lane);
+    }
+    if (wholes == heads) return;
+    __syncthreads();
+    for (uint32_t hs = heads & ~wholes; hs; hs &= hs - 1) {
+        const AttFrag g = frags[__ffs(hs) - 1];
+        if (!sh_last[g.item < cta0 ? 0 : 1]) continue;
+        const int c0 = (int)(g.item / share), c1 = (int)((g.item + g.tiles - 1) / share);
+        const AttSeq s = att_seq<RB>(a, g.seq);
+        auto part_of = [&](int k) { return a.partial + ((size_t)k * 2 + (k == c0 ? 1 : 0)) * C::GSlot; };
+        __syncthreads();
+        for (int r = warp; r < RB; r += W + 1) {
+            float ms[C::MaxCtas / 32], mx = -INFINITY, lt = 0.f;
+#pragma unroll
+            for (int i = 0; i < C::MaxCtas / 32; ++i) {
+                const int k = c0 + lane + 32 * i;
+                ms[i] = k <= c1 ? __ldcg(part_of(k) + RB * D + r) : -INFINITY;
+                mx = fmaxf(mx, ms[i]);
             }
-            __syncthreads();
-            if (sh_last) {
-                auto part_of = [&](int k) { return a.partial + ((size_t)k * 2 + (k == c0 ? 1 : 0)) * C::GSlot; };
-                for (int r = warp; r < RB; r += W) {
-                    float ms[C::MaxCtas / 32], mx = -INFINITY, lt = 0.f;
 #pragma unroll
-                    for (int i = 0; i < C::MaxCtas / 32; ++i) {
-                        const int k = c0 + lane + 32 * i;
-                        ms[i] = k <= c1 ? __ldcg(part_of(k) + RB * D + r) : -INFINITY;
-                        mx = fmaxf(mx, ms[i]);
-                    }
+            for (int o = 1; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
 #pragma unroll
-                    for (int o = 1; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            for (int i = 0; i < C::MaxCtas / 32; ++i) {
+                const int k = c0 + lane + 32 * i;
+                if (k > c1) continue;
+                const float w = ms[i] == mx ? 1.f : ex2(ms[i] - mx);
+                lt = fmaf(w, __ldcg(part_of(k) + RB * D + RB + r), lt);
+                weights[r * C::MaxCtas + k - c0] = w;
+            }
 #pragma unroll
-                    for (int i = 0; i < C::MaxCtas / 32; ++i) {
-                        const int k = c0 + lane + 32 * i;
-                        if (k > c1) continue;
-                        const float w = ms[i] == mx ? 1.f : ex2(ms[i] - mx);
-                        lt = fmaf(w, __ldcg(part_of(k) + RB * D + RB + r), lt);
-                        weights[r * C::MaxCtas + k - c0] = w;
-                    }
-#pragma unroll
-                    for (int o = 1; o < 32; o <<= 1) lt += __shfl_xor_sync(0xffffffffu, lt, o);
-                    if (lane == 0) {
-                        stats[r] = mx;
-                        stats[RB + r] = lt;
-                    }
-                }
-                __syncthreads();
-                for (int i = threadIdx.x; i < Vecs; i += T) {
-                    const int r = i / (D / 4);
-                    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-                    for (int k = c0; k <= c1; ++k) {
-                        const float w = weights[r * C::MaxCtas + k - c0];
-                        const float4 v = __ldcg(reinterpret_cast<const float4*>(part_of(k)) + i);
-                        o.x = fmaf(w, v.x, o.x);
-                        o.y = fmaf(w, v.y, o.y);
-                        o.z = fmaf(w, v.z, o.z);
-                        o.w = fmaf(w, v.w, o.w);
-                    }
-                    *reinterpret_cast<float4*>(rowbuf + 4 * i) = o;
-                }
-                __syncthreads();
-                store_rows(s, fr, rows);
+            for (int o = 1; o < 32; o <<= 1) lt += __shfl_xor_sync(0xffffffffu, lt, o);
+            if (lane == 0) {
+                stats[r * 2 * W] = mx;
+                stats[(RB + r) * 2 * W] = lt;
             }
         }
         __syncthreads();
-        f = e;
+        for (int i = threadIdx.x; i < Vecs; i += T) {
+            const int r = i / (D / 4);
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+            for (int k = c0; k <= c1; ++k) {
+                const float w = weights[r * C::MaxCtas + k - c0];
+                const float4 v = __ldcg(reinterpret_cast<const float4*>(part_of(k)) + i);
+                o.x = fmaf(w, v.x, o.x);
+                o.y = fmaf(w, v.y, o.y);
+                o.z = fmaf(w, v.z, o.z);
+                o.w = fmaf(w, v.w, o.w);
+            }
+            *reinterpret_cast<float4*>(rowbuf + 4 * i) = o;
+        }
+        __syncthreads();
+        for (int r = warp; r < min(RB, s.n * a.group - g.rb * RB); r += W + 1) {
+            float o[E];
+#pragma unroll
+            for (int k = 0; k < E; ++k) o[k] = rowbuf[r * D + E * lane + k];
+            store_row<D, BF16>(a, o, stats[r * 2 * W], stats[(RB + r) * 2 * W], s.row0, g.rb * RB + r, g.head, lane);
+        }
     }
 }
 

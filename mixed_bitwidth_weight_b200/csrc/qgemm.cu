@@ -972,7 +972,7 @@ int launch_attend(KvAttend a, DeviceInfo* dev, bool* attr, cudaStream_t s) {
         *attr = true;
     }
     static_assert(C::MaxCtas * 4 <= kAttendTicketBytes, "a ticket for each CTA");
-    kv_attend_kernel<D, NT, BF16><<<std::min(dev->sms, C::MaxCtas), 32 * C::W, C::RingAt + C::W * a.ring_bytes, s>>>(a);
+    kv_attend_kernel<D, NT, BF16><<<std::min(dev->sms, C::MaxCtas), C::T, C::RingAt + C::W * a.ring_bytes, s>>>(a);
     return launch_status();
 }
 
