@@ -46,42 +46,40 @@ struct KvAttend {
     KvRows q, out;
     float* lse;  // [rows][q_heads] or null
     int32_t q_heads, group, window;
-    int32_t stages, stage_bytes, ring_bytes;  // of a warp's ring
+    int32_t stages, ring_bytes;  // of a warp's ring
     float scale;
     unsigned int* tickets;  // [CTAs], zero between calls
     float* partial;         // [CTAs][2] slots
 };
 
 constexpr int kAttMaxStages = 8;
-constexpr float kAttShift = 10.f;    // weights are 2^(x - m + 10)
-constexpr float kAttSlack = 4.f;     // the running maximum may be this far behind (log2)
+constexpr float kAttNone = -3.4e38f;  // the weights' offset before any token: below every finite score
 
 template <int D, int NT>
 struct AttCfg {
-    // warps that multiply (one more feeds them): 168 registers a thread with 11, 255 with 7
-    static constexpr int W = D * NT <= 128 ? 11 : 7;
-    static constexpr int T = 32 * (W + 1);
+    static constexpr int W = D * NT <= 128 ? 11 : 7;  // warps: 168 registers a thread with 11, 255 with 7
+    static constexpr int T = 32 * W;
     static constexpr int G = D / 32;
     static constexpr int RB = 8 * NT;                 // query rows of an item
     static constexpr int OS = D + 4;                  // row stride of a slot: conflict-free float4 stores
     static constexpr int SlotFloats = RB * OS + 2 * RB;
     static constexpr int SlotBytes = SlotFloats * 4;
     static constexpr int GSlot = RB * D + 2 * RB;     // floats of a global slot
-    // an item's rotated query: [nt][g][hi, lo][lane] 16 bytes, then zq [nt][g][8], f [nt][8]
+    // an item's rotated query: [nt][g][hi, lo][lane] 16 bytes, then zq [nt][g][8], f [nt][8];
+    // QN of them are shared by the CTA's warps
+    static constexpr int QN = D * NT <= 128 ? 6 : 4;
     static constexpr int QZero = NT * G * 256, QFactor = QZero + NT * G * 8;
     static constexpr int QFloats = QFactor + NT * 8, QBytes = QFloats * 4;
-    // shared memory: slots, query areas, stage descriptors, barriers, fragments, prefix sums, rings
+    // shared memory: slots, query areas, barriers, fragments, prefix sums, rings
     static constexpr int QAt = W * SlotBytes;
-    static constexpr int DescAt = (QAt + W * QBytes + 15) / 16 * 16;
-    static_assert(W * SlotBytes >= W * RB * D * 2, "the query rows of W items pass through the slots");
-    static constexpr int BarAt = DescAt + W * 8 * 16;
-    static constexpr int FragAt = BarAt + 2 * W * 8 * 8;  // full and empty barriers
-    static constexpr int PrefixAt = (FragAt + 2 * W * 24 + 15) / 16 * 16;
-    static constexpr int RowAt = PrefixAt;  // a row of each warp, once the prefix sums are read
-    static constexpr int RingAt = (PrefixAt + (T * 8 > 2 * D * W ? T * 8 : 2 * D * W) + 127) / 128 * 128;
+    static constexpr int BarAt = (QAt + QN * QBytes + 15) / 16 * 16;
+    static constexpr int FragAt = BarAt + W * 8 * 8;
+    static constexpr int PrefixAt = FragAt + 2 * W * 24;
+    static constexpr int RingAt = (PrefixAt + T * 8 + 127) / 128 * 128;
+    static_assert(W * SlotBytes >= QN * RB * D * 2, "the query rows of QN items pass through the slots");
     // the join's weights and row buffer lie over the query areas
     static constexpr int MaxCtas = 160;
-    static_assert(W * QBytes >= (RB * MaxCtas + RB * D + 2 * RB * 2 * W) * 4, "join buffers");
+    static_assert(QN * QBytes >= (RB * MaxCtas + RB * D + 2 * RB * 2 * W) * 4, "join buffers");
 };
 
 // a slot's fragment: tiles [a, b) of the item whose first tile is number `item`
@@ -98,13 +96,13 @@ QG_DEV void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// the first of a chain: starts at (c0, c1) for both row halves
+// the first of a chain
 QG_DEV void mma_f16_from(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1,
-                         float c0, float c1) {
+                         const float (&c)[4]) {
     asm(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%10,%11};"
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
         : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1));
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
 }
 
 QG_DEV uint32_t movm_trans(uint32_t a) {
@@ -229,7 +227,7 @@ QG_DEV void load_words(const uint8_t* part, int half, int lane, uint32_t (&w)[D 
 template <int D, int NT>
 struct AttQ {
     uint32_t hi[NT][D / 32][4], lo[NT][D / 32][4];
-    float zq[NT][D / 32][2];
+    float zq[NT][D / 32][4];  // an accumulator's four: rows r and r + 8 start alike
     float f[NT][2];  // factor of a score, log2 units
 };
 
@@ -302,7 +300,7 @@ QG_DEV void scores_tile(const uint8_t* rec, int lane, const AttQ<D, NT>& q, floa
                     for (int nt = 0; nt < NT; ++nt) {
                         if (step == 0)
                             mma_f16_from(c[h][nt][g], x[0], x[1], x[2], x[3], q.hi[nt][g][0], q.hi[nt][g][1],
-                                         q.zq[nt][g][0], q.zq[nt][g][1]);
+                                         q.zq[nt][g]);
                         else
                             mma_f16(c[h][nt][g], x[0], x[1], x[2], x[3], q.hi[nt][g][2], q.hi[nt][g][3]);
                     }
@@ -334,6 +332,27 @@ QG_DEV void scores_tile(const uint8_t* rec, int lane, const AttQ<D, NT>& q, floa
     }
 }
 
+// A rotated row's power-of-two scale (largest magnitude into [2^14, 2^15), so that
+// both fp16 parts keep their bits; the score scale's sign goes with it), -z 2^-24,
+// and the factor that turns a score into log2 units.  The factor is positive, so
+// masked scores stay -inf and maxima can be taken before it.
+struct AttRowScale {
+    float up, zero, f;
+};
+template <int D>
+QG_DEV AttRowScale att_row_scale(const KvAttend& a, float amax) {
+    int e = (int)(__float_as_uint(amax) >> 23) - 127;  // 128 for infinity: no scaling then
+    e = e >= 128 ? 14 : max(e, -100);
+    AttRowScale r;
+    r.up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
+    if (a.scale < 0.f) r.up = -r.up;
+    r.zero = -(float)(1 << (a.pg.kb - 1)) * 5.9604644775390625e-8f;
+    r.f = fmaxf(fabsf(a.scale) * (1.4426950408889634f / (float)D) * 16777216.f *
+                    __uint_as_float((uint32_t)(127 - 14 + e) << 23),
+                1e-30f);
+    return r;
+}
+
 // Rotate query row n (of 8) of row tile nt, a warp to a row, split it into its two
 // parts and put them where the B operand's lanes read them (row n's dims
 // 32 g + 8 j + i are lane 4 n + j's, pair i % 4, half i / 4).  p: the row in shared memory.
@@ -345,22 +364,19 @@ QG_DEV void rotate_query(const KvAttend& a, const uint16_t* p, float* area, int 
 #pragma unroll
     for (int i = 0; i < E; ++i) x[i] = kv_to_float<BF16>(p[E * lane + i]);
     fwht_warp<E>(x, lane);
-    // largest magnitude into [2^14, 2^15): both fp16 parts keep their bits
     float amax = 0.f;
 #pragma unroll
     for (int i = 0; i < E; ++i) amax = fmaxf(amax, fabsf(x[i]));
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    int e = (int)(__float_as_uint(amax) >> 23) - 127;  // 128 for infinity: no scaling then
-    e = e >= 128 ? 14 : max(e, -100);
-    const float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
+    const AttRowScale rs = att_row_scale<D>(a, amax);
     uint16_t* out = reinterpret_cast<uint16_t*>(area);
     float sum = 0.f;
     const int g = E * lane / 32;
 #pragma unroll
     for (int i = 0; i < E; ++i) {
         const int d = E * lane + i, pair = d & 3;
-        const float v = x[i] * up, vd = v * __uint_as_float((uint32_t)(127 - field_at(a.pg.kb, pair)) << 23);
+        const float v = x[i] * rs.up, vd = v * __uint_as_float((uint32_t)(127 - field_at(a.pg.kb, pair)) << 23);
         const __half hi = __float2half_rn(vd), lo = __float2half_rn(vd - __half2float(hi));
         const int at = ((((nt * G + g) * 2) * 32 + 4 * n + ((d & 31) >> 3)) * 4 + pair) * 2 + ((d >> 2) & 1);
         out[at] = __half_as_ushort(hi);
@@ -369,11 +385,87 @@ QG_DEV void rotate_query(const KvAttend& a, const uint16_t* p, float* area, int 
     }
 #pragma unroll
     for (int o = 1; o < 32 / E; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (lane % (32 / E) == 0)
-        area[C::QZero + (nt * G + g) * 8 + n] = -(float)(1 << (a.pg.kb - 1)) * 5.9604644775390625e-8f * sum;
-    if (lane == 0)
-        area[C::QFactor + nt * 8 + n] = a.scale * (1.4426950408889634f / (float)D) * 16777216.f *
-                                        __uint_as_float((uint32_t)(127 - 14 + e) << 23);
+    if (lane % (32 / E) == 0) area[C::QZero + (nt * G + g) * 8 + n] = rs.zero * sum;
+    if (lane == 0) area[C::QFactor + nt * 8 + n] = rs.f;
+}
+
+// The same for all rows of an item by one warp for itself, straight into the B
+// operand's registers: lane 4 n + j rotates its share of row n, strides 1, 2, 4 and
+// 32 .. within the lane, 8 and 16 between the four lanes of the row.
+template <int D, int NT, bool BF16>
+QG_DEV void rotate_queries(const KvAttend& a, int row0, int rows, int r_base, int head, int lane, AttQ<D, NT>& q) {
+    constexpr int G = D / 32;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        const int r = r_base + nt * 8 + (lane >> 2);
+        float x[G][8];
+#pragma unroll
+        for (int g = 0; g < G; ++g)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[g][i] = 0.f;
+        if (r < rows) {
+            const int tok = r / a.group, hq = head * a.group + (r - tok * a.group);
+            const uint16_t* p = reinterpret_cast<const uint16_t*>(a.q.p) + (row0 + tok) * a.q.row + hq * a.q.head;
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+                const uint4 u = __ldg(reinterpret_cast<const uint4*>(p + 32 * g + 8 * (lane & 3)));
+                const uint32_t v[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    x[g][i] = kv_to_float<BF16>((uint16_t)((i & 1) ? v[i / 2] >> 16 : v[i / 2] & 0xffff));
+            }
+        }
+        float amax = 0.f;
+#pragma unroll
+        for (int st = 1; st < D; st <<= 1)
+#pragma unroll
+            for (int g = 0; g < G; ++g)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    if (st < 8) {
+                        if (i & st) continue;
+                        const float u = x[g][i], v = x[g][i | (st & 7)];
+                        x[g][i] = u + v;
+                        x[g][i | (st & 7)] = u - v;
+                    } else if (st < 32) {
+                        const float o = __shfl_xor_sync(0xffffffffu, x[g][i], st / 8);
+                        x[g][i] = (lane & (st / 8)) ? o - x[g][i] : x[g][i] + o;
+                    } else {
+                        if (g & (st / 32)) continue;
+                        const float u = x[g][i], v = x[(g | (st / 32)) % G][i];
+                        x[g][i] = u + v;
+                        x[(g | (st / 32)) % G][i] = u - v;
+                    }
+                }
+#pragma unroll
+        for (int g = 0; g < G; ++g)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(x[g][i]));
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+        const AttRowScale rs = att_row_scale<D>(a, amax);
+        const int src = (lane & 3) * 8;  // lane of row 2 j
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+            float sum = 0.f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float u = x[g][i] * rs.up, v = x[g][i + 4] * rs.up;
+                const float dn = __uint_as_float((uint32_t)(127 - field_at(a.pg.kb, i)) << 23);
+                const __half2 hi = __floats2half2_rn(u * dn, v * dn);
+                q.hi[nt][g][i] = h2_bits(hi);
+                q.lo[nt][g][i] = h2_bits(__floats2half2_rn(u * dn - __low2float(hi), v * dn - __high2float(hi)));
+                sum += u + v;
+            }
+            sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+            sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+            sum *= rs.zero;
+            q.zq[nt][g][0] = q.zq[nt][g][2] = __shfl_sync(0xffffffffu, sum, src);
+            q.zq[nt][g][1] = q.zq[nt][g][3] = __shfl_sync(0xffffffffu, sum, src + 4);
+        }
+        q.f[nt][0] = __shfl_sync(0xffffffffu, rs.f, src);
+        q.f[nt][1] = __shfl_sync(0xffffffffu, rs.f, src + 4);
+    }
 }
 
 template <int D, int NT>
@@ -389,8 +481,8 @@ QG_DEV void load_queries(const float* area, int lane, AttQ<D, NT>& q) {
             q.hi[nt][g][0] = h.x, q.hi[nt][g][1] = h.y, q.hi[nt][g][2] = h.z, q.hi[nt][g][3] = h.w;
             q.lo[nt][g][0] = l.x, q.lo[nt][g][1] = l.y, q.lo[nt][g][2] = l.z, q.lo[nt][g][3] = l.w;
             const float2 z = *reinterpret_cast<const float2*>(area + C::QZero + (nt * G + g) * 8 + 2 * (lane & 3));
-            q.zq[nt][g][0] = z.x;
-            q.zq[nt][g][1] = z.y;
+            q.zq[nt][g][0] = q.zq[nt][g][2] = z.x;
+            q.zq[nt][g][1] = q.zq[nt][g][3] = z.y;
         }
         const float2 v = *reinterpret_cast<const float2*>(area + C::QFactor + nt * 8 + 2 * (lane & 3));
         q.f[nt][0] = v.x;
@@ -402,55 +494,60 @@ QG_DEV void load_queries(const float* area, int lane, AttQ<D, NT>& q) {
 // acc += (codes of V) x (weights): half a tile.  p[nt][k]: weights of tokens
 // 16 half + 8 k + 2 j + {0, 1} for row n = lane / 4.
 template <int D, int NT, int B, bool Masked>
-QG_DEV void output_half(const uint8_t* part, int half, int lane, __half2 es, const uint32_t (&p)[NT][2],
+QG_DEV void output_half(const uint8_t* part, int half, int lane, const uint32_t (&p)[NT][2],
                         float (&acc)[NT][D / 16][4]) {
     constexpr int G = D / 32, NW = D * B / 64, UT = D / 64 * 8 * B;  // bits of a token's units
     uint32_t w[NW];
     load_words<D, B>(part, half, lane, w);
     const uint8_t* scales = part + 4 * D * B + ((lane & 3) * G * 8 + 4 * half) * 2;
+    constexpr int GB = 1;
 #pragma unroll
-    for (int g = 0; g < G; ++g) {
-        const uint2 su = *reinterpret_cast<const uint2*>(scales + g * 16);
-        const __half2 s0 = __hmul2(bits_h2(su.x), es), s1 = __hmul2(bits_h2(su.y), es);
-        uint32_t b0[NT], b1[NT];
+    for (int g0 = 0; g0 < G; g0 += GB) {
+        uint32_t b0[GB][NT], b1[GB][NT];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            b0[nt] = h2_bits(__hmul2(bits_h2(p[nt][0]), s0));
-            b1[nt] = h2_bits(__hmul2(bits_h2(p[nt][1]), s1));
-        }
-        if constexpr (Masked) {  // a weight of 0 is 0 whatever the scale it meets
+        for (int gi = 0; gi < GB; ++gi) {
+            const int g = g0 + gi;
+            const uint2 su = *reinterpret_cast<const uint2*>(scales + g * 16);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                b0[nt] &= __hneu2_mask(bits_h2(p[nt][0]), bits_h2(0));
-                b1[nt] &= __hneu2_mask(bits_h2(p[nt][1]), bits_h2(0));
+                b0[gi][nt] = h2_bits(__hmul2(bits_h2(p[nt][0]), bits_h2(su.x)));
+                b1[gi][nt] = h2_bits(__hmul2(bits_h2(p[nt][1]), bits_h2(su.y)));
+                if constexpr (Masked) {  // a weight of 0 is 0 whatever the scale it meets
+                    b0[gi][nt] &= __hneu2_mask(bits_h2(p[nt][0]), bits_h2(0));
+                    b1[gi][nt] &= __hneu2_mask(bits_h2(p[nt][1]), bits_h2(0));
+                }
             }
         }
-        const int unit = (g >> 1) * 8 * B + (g & 1) * 4 * B;  // this group's four codes in a token's units
-        uint32_t f[2][4];
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const int t0 = (2 * k) * UT + unit, t1 = (2 * k + 1) * UT + unit;
-            if constexpr (B <= 4) {
-                const uint32_t x = halves_from(w, t0, t1, 4 * B);
-                f[k][0] = field<B, 0>(x);
-                f[k][1] = field<B, 1>(x);
-                f[k][2] = field<B, 2 % Fld<B>::N>(x);
-                f[k][3] = field<B, 3 % Fld<B>::N>(x);
-            } else {
-                const uint32_t x = halves_from(w, t0, t1, 2 * B), y = halves_from(w, t0 + 2 * B, t1 + 2 * B, 2 * B);
-                f[k][0] = field<B, 0>(x);
-                f[k][1] = field<B, 1>(x);
-                f[k][2] = field<B, 0>(y);
-                f[k][3] = field<B, 1>(y);
+        for (int gi = 0; gi < GB; ++gi) {
+            const int g = g0 + gi;
+            const int unit = (g >> 1) * 8 * B + (g & 1) * 4 * B;  // this group's four codes in a token's units
+            uint32_t f[2][4];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int t0 = (2 * k) * UT + unit, t1 = (2 * k + 1) * UT + unit;
+                if constexpr (B <= 4) {
+                    const uint32_t x = halves_from(w, t0, t1, 4 * B);
+                    f[k][0] = field<B, 0>(x);
+                    f[k][1] = field<B, 1>(x);
+                    f[k][2] = field<B, 2 % Fld<B>::N>(x);
+                    f[k][3] = field<B, 3 % Fld<B>::N>(x);
+                } else {
+                    const uint32_t x = halves_from(w, t0, t1, 2 * B), y = halves_from(w, t0 + 2 * B, t1 + 2 * B, 2 * B);
+                    f[k][0] = field<B, 0>(x);
+                    f[k][1] = field<B, 1>(x);
+                    f[k][2] = field<B, 0>(y);
+                    f[k][3] = field<B, 1>(y);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    f[k][i] = h2_bits(__hsub2(bits_h2(f[k][i]), bits_h2(Fld<B>::zero(i % Fld<B>::N))));
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                f[k][i] = h2_bits(__hsub2(bits_h2(f[k][i]), bits_h2(Fld<B>::zero(i % Fld<B>::N))));
-        }
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            mma_f16(acc[nt][2 * g], f[0][0], f[0][1], f[1][0], f[1][1], b0[nt], b1[nt]);
-            mma_f16(acc[nt][2 * g + 1], f[0][2], f[0][3], f[1][2], f[1][3], b0[nt], b1[nt]);
+            for (int nt = 0; nt < NT; ++nt) {
+                mma_f16(acc[nt][2 * g], f[0][0], f[0][1], f[1][0], f[1][1], b0[gi][nt], b1[gi][nt]);
+                mma_f16(acc[nt][2 * g + 1], f[0][2], f[0][3], f[1][2], f[1][3], b0[gi][nt], b1[gi][nt]);
+            }
         }
     }
 }
@@ -551,9 +648,6 @@ QG_DEV void att_next(const KvAttend& a, AttCursor& c, bool more) {
     } while (c.s.nrb == 0 && c.b + 1 < a.bt.num_seqs);
 }
 
-constexpr int kDescFirst = 1, kDescLast = 2, kDescSkip = 4, kDescHead = 8, kDescTail = 16;
-// First / Last: of the item within this warp's run; Head / Tail: of the item itself
-
 // rotate back, divide and store one row held by a warp (E consecutive dims a lane)
 template <int D, bool BF16>
 QG_DEV void store_row(const KvAttend& a, float (&o)[D / 32], float m, float l, int row0, int r, int head, int lane) {
@@ -573,7 +667,7 @@ QG_DEV void store_row(const KvAttend& a, float (&o)[D / 32], float m, float l, i
             *reinterpret_cast<uint2*>(p + i) = make_uint2(v[i] | (uint32_t)v[i + 1] << 16, v[i + 2] | (uint32_t)v[i + 3] << 16);
     }
     if (a.lse && lane == 0)
-        a.lse[(int64_t)(row0 + tok) * a.q_heads + hq] = (m + log2f(l) - kAttShift) * 0.6931471805599453f;
+        a.lse[(int64_t)(row0 + tok) * a.q_heads + hq] = (m + log2f(l)) * 0.6931471805599453f;
 }
 
 template <int D, int NT, bool BF16>
@@ -581,17 +675,17 @@ __global__ void __launch_bounds__(AttCfg<D, NT>::T, 1) kv_attend_kernel(KvAttend
     using C = AttCfg<D, NT>;
     constexpr int W = C::W, G = C::G, RB = C::RB, E = D / 32, T = C::T;
     extern __shared__ __align__(1024) uint8_t smem[];
-    __shared__ long long sh_total[W + 1];
+    __shared__ long long sh_total[W];
     __shared__ int sh_last[2];
-    __shared__ int sh_dead;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int rec_bytes = kv_record_bytes<D>(a.pg.kb, a.pg.vb), k_bytes = 4 * D * a.pg.kb + 2 * D;
     float* slots = reinterpret_cast<float*>(smem);
     float* areas = reinterpret_cast<float*>(smem + C::QAt);
-    uint64_t* full0 = reinterpret_cast<uint64_t*>(smem + C::BarAt);
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::BarAt) + warp * kAttMaxStages;
     AttFrag* frags = reinterpret_cast<AttFrag*>(smem + C::FragAt);
     long long* prefix = reinterpret_cast<long long*>(smem + C::PrefixAt);
     uint8_t* rings = smem + C::RingAt;
+    uint8_t* ring = rings + warp * a.ring_bytes;
 
     // ---- the call's work, this CTA's and each warp's share
     const int chunk = (a.bt.num_seqs + T - 1) / T;
@@ -607,14 +701,13 @@ __global__ void __launch_bounds__(AttCfg<D, NT>::T, 1) kv_attend_kernel(KvAttend
         if (lane >= o) inc += v;
     }
     if (lane == 31) sh_total[warp] = inc;
-    for (int i = threadIdx.x; i < 2 * W * kAttMaxStages; i += T) mbar_init(&full0[i], 1);
+    if (lane < kAttMaxStages) mbar_init(&full[lane], 1);
     if (threadIdx.x < 2 * W) frags[threadIdx.x].tiles = 0;
-    if (threadIdx.x == 0) sh_dead = 0;
     fence_mbar_init();
     __syncthreads();
     long long before = 0, total = 0;
 #pragma unroll
-    for (int w = 0; w <= W; ++w) {
+    for (int w = 0; w < W; ++w) {
         if (w < warp) before += sh_total[w];
         total += sh_total[w];
     }
@@ -624,203 +717,140 @@ __global__ void __launch_bounds__(AttCfg<D, NT>::T, 1) kv_attend_kernel(KvAttend
     const long long share = max((total + gridDim.x - 1) / gridDim.x, 2ll * W);
     const long long cta0 = min(share * blockIdx.x, total), cta1 = min(cta0 + share, total);
     if (cta0 >= cta1) return;
-    const long long per = (cta1 - cta0 + W - 1) / W;
+    // warp w's first tile: shares differ by one at most
+    const int cta_tiles = (int)(cta1 - cta0);
+    const long long w0 = cta0 + (cta_tiles / W) * warp + min(warp, cta_tiles % W);
+    int count = cta_tiles / W + (warp < cta_tiles % W ? 1 : 0);
 
-    if (warp == W) {
-        // ---- the feeding warp: lane w walks warp w's run and keeps its ring full.  Copies
-        // alternate, a tile's K part and its V part; a stage is free again when its warp
-        // has arrived on the empty barrier.
-        const long long w0 = min(cta0 + per * lane, cta1);
-        long long left = lane < W ? min(w0 + per, cta1) - w0 : 0;
-        AttCursor pc;
-        if (left > 0) att_seek<RB>(a, prefix, T, chunk, w0, pc);
-        named_bar_sync(1, T);  // the prefix sums are read
-        uint64_t* full = full0 + min(lane, W - 1) * kAttMaxStages;
-        uint64_t* empty = full + W * kAttMaxStages;
-        uint8_t* ring = rings + min(lane, W - 1) * a.ring_bytes;
-        int4* descs = reinterpret_cast<int4*>(smem + C::DescAt) + min(lane, W - 1) * kAttMaxStages;
-        const int lps = 31 - __clz(a.pg.page_size / kTileTokens);  // log2 tiles per page
-        // a table entry, -1 where there is none
-        auto page_at = [&](int b, const AttSeq& s, int pi) {
-            return pi < a.bt.max_pages && ((int64_t)pi << lps) * kTileTokens < s.len
-                       ? a.bt.table[b * a.bt.table_stride + pi]
-                       : -1;
-        };
-        int stage = 0, rounds = 0, page_left = 0, next_page = 0;
-        bool value_next = false, has = false, first_of_run = true;
-        const uint8_t* src = nullptr;
-        uint32_t idle = 0;
-        uint64_t idle_since = 0;
-        while (__any_sync(0xffffffffu, left > 0)) {
-            const bool dead = *reinterpret_cast<volatile int*>(&sh_dead) != 0;
-            const bool go = left > 0 && (rounds == 0 || dead || mbar_try_wait(&empty[stage], (rounds - 1) & 1));
-            if (go) {
-                if (!value_next) {
-                    if (page_left == 0 || pc.tile == 0) {
-                        const int t = pc.s.t0 + pc.tile, pi = t >> lps, in = t & ((1 << lps) - 1);
-                        const int page = pc.tile == 0 || first_of_run ? page_at(pc.b, pc.s, pi) : next_page;
-                        next_page = page_at(pc.b, pc.s, pi + 1);  // read ahead: here when it is needed
-                        page_left = (1 << lps) - in;
-                        has = pc.s.len > 0 && page >= 0 && page < a.pg.num_pages;
-                        if (pc.s.len > 0 && !has) set_dev_error(QGEMM_DEV_BAD_PAGE);
-                        src = a.pg.base + page * a.pg.page_bytes + (int64_t)((pc.h << lps) + in) * rec_bytes;
-                    }
-                    const bool last = pc.tile + 1 == pc.s.tiles;
-                    const int flags = (first_of_run || pc.tile == 0 ? kDescFirst : 0) |
-                                      (left == 1 || last ? kDescLast : 0) | (has ? 0 : kDescSkip) |
-                                      (pc.tile == 0 ? kDescHead : 0) | (last ? kDescTail : 0);
-                    first_of_run = false;
-                    descs[stage] = make_int4(pc.b, pc.h | flags << 16, pc.rb, pc.tile);
-                }
-                const int bytes = value_next ? rec_bytes - k_bytes : k_bytes;
-                if (has && !dead) {
-                    mbar_arrive_expect_tx(&full[stage], bytes);
-                    bulk_g2s(ring + stage * a.stage_bytes, src, bytes, &full[stage]);
-                } else {
-                    mbar_arrive(&full[stage]);
-                }
-                src += bytes;
-                if (value_next) {
-                    --page_left;
-                    --left;
-                    att_next<RB>(a, pc, left > 0);
-                }
-                value_next = !value_next;
-                if (++stage == a.stages) {
-                    stage = 0;
-                    ++rounds;
-                }
+    // ---- Walk the CTA's first items.  Where it has no more than QN all warps share their
+    // rotated queries: each warp fetches some of the rows here, ahead of the cache's tiles,
+    // and rotates them once those are on their way.
+    uint16_t* raw = reinterpret_cast<uint16_t*>(smem);  // [item][RB][D], over the slots
+    auto fetch_row = [&](const AttSeq& s, int head, int rb, int r, uint16_t* dst) {
+        r += rb * RB;
+        const uint16_t* p = nullptr;
+        if (r < s.n * a.group) {
+            const int tok = r / a.group, hq = head * a.group + (r - tok * a.group);
+            p = reinterpret_cast<const uint16_t*>(a.q.p) + (s.row0 + tok) * a.q.row + hq * a.q.head;
+        }
+        for (int i = lane * 8; i < D; i += 256) {  // 16 bytes a lane
+            if (p)
+                cp_async16(dst + i, p + i);
+            else
+                *reinterpret_cast<uint4*>(dst + i) = make_uint4(0, 0, 0, 0);
+        }
+    };
+    AttCursor pc, cc;  // the place of the copies, the place of the sums
+    int my_item = 0, items = 0;
+    bool found = count == 0;
+    {
+        AttCursor c;
+        att_seek<RB>(a, prefix, T, chunk, cta0, c);
+        long long at = cta0 - c.tile;
+        for (; items <= C::QN && at < cta1; ++items) {
+            if (items < C::QN)
+                for (int r = (warp + W - items * RB % W) % W; r < RB; r += W)
+                    fetch_row(c.s, c.h, c.rb, r, raw + (items * RB + r) * D);
+            if (!found && w0 < at + c.s.tiles) {
+                found = true;
+                my_item = items;
+                pc = c;
+                pc.tile = (int)(w0 - at);
             }
-            if (__any_sync(0xffffffffu, go)) {
-                idle = 0;
-            } else if ((++idle & 1023u) == 0) {  // a bounded wait: the warps' own waits give up after a second
-                const uint64_t now = globaltimer_ns();
-                if (idle == 1024) idle_since = now;
-                if (__any_sync(0xffffffffu, now - idle_since > 2000000000ull)) break;
+            at += c.s.tiles;
+            c.tile = c.s.tiles - 1;
+            att_next<RB>(a, c, at < cta1);
+        }
+    }
+    const bool shared_q = items <= C::QN;
+    if (!found) att_seek<RB>(a, prefix, T, chunk, w0, pc);
+    cc = pc;
+
+    // ---- The ring: whole records, each warp its own.
+    const int lps = 31 - __clz(a.pg.page_size / kTileTokens);  // log2 tiles per page
+    int page_base = 0, page_b = -1, page_id = 0;               // lane i: page page_base + i of sequence page_b
+    int left = count;
+    uint32_t bad = 0;  // stages whose tile has no page
+    bool dead = false;
+    auto issue = [&](int s) {
+        const int t = pc.s.t0 + pc.tile, pi = t >> lps;
+        if (page_b != pc.b || (uint32_t)(pi - page_base) >= 32u) {
+            page_b = pc.b;
+            page_base = pi;
+            const int i = pi + lane;
+            page_id = i < a.bt.max_pages && ((int64_t)i << lps) * kTileTokens < pc.s.len
+                          ? a.bt.table[pc.b * a.bt.table_stride + i]
+                          : -1;
+        }
+        const int page = __shfl_sync(0xffffffffu, page_id, pi - page_base);
+        const bool has = (uint32_t)page < (uint32_t)a.pg.num_pages && pc.s.len > 0;
+        bad = has ? bad & ~(1u << s) : bad | 1u << s;
+        if (lane == 0) {
+            if (has && !dead) {
+                const uint8_t* src = a.pg.base + page * a.pg.page_bytes +
+                                     (int64_t)((pc.h << lps) + (t & ((1 << lps) - 1))) * rec_bytes;
+                mbar_arrive_expect_tx(&full[s], rec_bytes);
+                bulk_g2s(ring + s * rec_bytes, src, rec_bytes, &full[s]);
+            } else {
+                if (!has && pc.s.len > 0) set_dev_error(QGEMM_DEV_BAD_PAGE);
+                mbar_arrive(&full[s]);
             }
         }
-        if (*reinterpret_cast<volatile int*>(&sh_dead) != 0 && lane < W) {
-            // copies still in flight: each stage's last one
-            for (int s = 0; s < a.stages; ++s) {
-                const int r = s < stage ? rounds : rounds - 1;
-                if (r >= 0) mbar_wait(&full[s], r & 1);
-            }
-        }
-        __syncwarp();
-    } else {
-        const long long w0 = min(cta0 + per * warp, cta1);
-        const int count = (int)(min(w0 + per, cta1) - w0);
-        // Where the CTA has no more than W items all warps share their rotated queries: each
-        // warp fetches and rotates some of the rows.
-        uint16_t* raw = reinterpret_cast<uint16_t*>(smem);  // [item][RB][D], over the slots
-        auto fetch_row = [&](const AttSeq& s, int head, int rb, int r, uint16_t* dst) {
-            r += rb * RB;
-            const uint16_t* p = nullptr;
-            if (r < s.n * a.group) {
-                const int tok = r / a.group, hq = head * a.group + (r - tok * a.group);
-                p = reinterpret_cast<const uint16_t*>(a.q.p) + (s.row0 + tok) * a.q.row + hq * a.q.head;
-            }
-            for (int i = lane * 8; i < D; i += 256) {  // 16 bytes a lane
-                if (p)
-                    cp_async16(dst + i, p + i);
-                else
-                    *reinterpret_cast<uint4*>(dst + i) = make_uint4(0, 0, 0, 0);
-            }
-        };
-        int my_item = 0, items = 0;
-        {
-            AttCursor c;
-            att_seek<RB>(a, prefix, T, chunk, cta0, c);
-            long long at = cta0 - c.tile;
-            for (; items <= W && at < cta1; ++items) {
-                if (items < W)
-                    for (int r = (warp + W - items % W * RB % W) % W; r < RB; r += W)
-                        fetch_row(c.s, c.h, c.rb, r, raw + (items * RB + r) * D);
-                if (w0 >= at && w0 < at + c.s.tiles) my_item = items;
-                at += c.s.tiles;
-                c.tile = c.s.tiles - 1;
-                att_next<RB>(a, c, at < cta1);
-            }
-        }
-        const bool shared_q = items <= W;
-        cp_async_wait_all();
-        __syncwarp();
+        --left;
+        att_next<RB>(a, pc, left > 0);
+    };
+    for (int i = 0; i < a.stages && left > 0; ++i) issue(i);
+
+    // ---- rotated queries: rows of the CTA's items dealt out to the warps
+    cp_async_wait_all();
+    __syncwarp();
+    if (shared_q)
+        for (int i = 0; i < items; ++i)
+            for (int r = (warp + W - i * RB % W) % W; r < RB; r += W)
+                rotate_query<D, NT, BF16>(a, raw + (i * RB + r) * D, areas + i * C::QFloats, r >> 3, r & 7, lane);
+    __syncthreads();
+
+    // ---- one warp's run, item by item
+    AttQ<D, NT> q;
+    float acc[NT][2 * G][4], mo[NT][2], l[NT][2];  // weights are 2^(x - mo)
+    int stage = 0, parity = 0;
+    const int j = lane & 3, r8 = lane >> 2;
+    for (long long at = w0; count > 0;) {
+        const AttSeq& cs = cc.s;
+        const int n_tiles = min(count, cs.tiles - cc.tile);  // of this item, here
+        const int rows = cs.n * a.group, r_base = cc.rb * RB;
         if (shared_q)
-            for (int i = 0; i < items; ++i)
-                for (int r = (warp + W - i % W * RB % W) % W; r < RB; r += W)
-                    rotate_query<D, NT, BF16>(a, raw + (i * RB + r) * D, areas + i * C::QFloats, r >> 3, r & 7, lane);
-        named_bar_sync(1, T);
-
-        // ---- one warp's run
-        uint64_t* full = full0 + warp * kAttMaxStages;
-        uint64_t* empty = full + W * kAttMaxStages;
-        const uint8_t* ring = rings + warp * a.ring_bytes;
-        const int4* descs = reinterpret_cast<const int4*>(smem + C::DescAt) + warp * kAttMaxStages;
-        AttQ<D, NT> q;
-        float acc[NT][2 * G][4], m[NT][2], mo[NT][2], l[NT][2];
-        AttSeq cs{};
-        int qpos[NT][2], lo_pos = 0, hi_pos = 0, E2 = -14;
-        bool frag_head = false, dead = false;
-        int stage = 0, parity = 0;
-        const int j = lane & 3, r8 = lane >> 2;
-        auto arrived = [&] {
-            if (!dead && !__all_sync(0xffffffffu, mbar_wait(&full[stage], parity))) {
-                dead = true;  // the feeding warp stops copying
-                if (lane == 0) *reinterpret_cast<volatile int*>(&sh_dead) = 1;
+            load_queries<D, NT>(areas + my_item * C::QFloats, lane, q);
+        else
+            rotate_queries<D, NT, BF16>(a, cs.row0, rows, r_base, cc.h, lane, q);
+        ++my_item;
+        const int lo_pos = cs.pos0 + r_base / a.group;
+        const int hi_pos = cs.pos0 + (min(r_base + RB, rows) - 1) / a.group;
+        int qpos[NT][2], ve = 0;  // ve: exponent of the largest V scale, 0 at least
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                qpos[nt][c] = cs.pos0 + (r_base + 8 * nt + 2 * j + c) / a.group;
+                mo[nt][c] = kAttNone;
+                l[nt][c] = 0.f;
             }
-        };
-        auto release = [&] {
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&empty[stage]);
-            if (++stage == a.stages) {
-                stage = 0;
-                parity ^= 1;
-            }
-        };
-        for (int done = 0; done < count; ++done) {
-            arrived();
-            const int4 d = descs[stage];
-            const int flags = d.y >> 16, head = d.y & 0xffff;
-            if (flags & kDescFirst) {
-                cs = att_seq<RB>(a, d.x);
-                const int rows = cs.n * a.group, r_base = d.z * RB;
-                if (!shared_q) {
-                    uint16_t* row = reinterpret_cast<uint16_t*>(smem + C::RowAt) + warp * D;
-                    for (int r = 0; r < RB; ++r) {
-                        __syncwarp();
-                        fetch_row(cs, head, d.z, r, row);
-                        cp_async_wait_all();
-                        __syncwarp();
-                        rotate_query<D, NT, BF16>(a, row, areas + warp * C::QFloats, r >> 3, r & 7, lane);
-                    }
-                    __syncwarp();
-                }
-                load_queries<D, NT>(areas + (shared_q ? my_item : warp) * C::QFloats, lane, q);
-                ++my_item;
-                lo_pos = cs.pos0 + r_base / a.group;
-                hi_pos = cs.pos0 + (min(r_base + RB, rows) - 1) / a.group;
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        qpos[nt][c] = cs.pos0 + (r_base + 8 * nt + 2 * j + c) / a.group;
-                        m[nt][c] = -INFINITY;
-                        mo[nt][c] = -kAttShift;
-                        l[nt][c] = 0.f;
-                    }
+            for (int i = 0; i < 2 * G; ++i)
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int i = 0; i < 2 * G; ++i)
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) acc[nt][i][c] = 0.f;
-                E2 = -14;
-                frag_head = flags & kDescHead;
-            }
-            const bool skip = (flags & kDescSkip) || dead;
+                for (int c = 0; c < 4; ++c) acc[nt][i][c] = 0.f;
+#pragma unroll 1
+        for (int it = 0; it < n_tiles; ++it) {
+            if (!mbar_try_wait(&full[stage], parity) && !dead && !mbar_wait(&full[stage], parity)) dead = true;
+            // (given up: no copy is issued any more and nothing is waited for; the run goes on over
+            // whatever the ring holds, and the error word says so)
             float s[2][NT][4];
-            if (!skip) {
-                const uint8_t* rec = ring + stage * a.stage_bytes;
+            const uint8_t* rec = ring + stage * rec_bytes;
+            const uint8_t* vpart = rec + k_bytes;
+            const int t_first = (cs.t0 + cc.tile + it) * kTileTokens;
+            {
                 switch (a.pg.kb) {
 #define QG_SCORES(B)                            \
     case B:                                     \
@@ -835,18 +865,12 @@ __global__ void __launch_bounds__(AttCfg<D, NT>::T, 1) kv_attend_kernel(KvAttend
 #undef QG_SCORES
                 }
             }
-            release();
-            arrived();
-            if (!skip && !dead) {
-                const uint8_t* vpart = ring + stage * a.stage_bytes;
-                const int t_first = (cs.t0 + d.w) * kTileTokens;
-                const bool masked = t_first + kTileTokens - 1 > lo_pos || (a.window > 0 && t_first <= hi_pos - a.window);
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) s[h][nt][c] *= q.f[nt][c & 1];
+            {
+                // a tile without a page shows nothing
+                const bool none = bad >> stage & 1;
+                const bool masked = t_first + kTileTokens - 1 > lo_pos || none ||
+                                    (a.window > 0 && t_first <= hi_pos - a.window);
+                const int last = none ? -1 : hi_pos - t_first;  // last slot that any row sees
                 if (masked) {
 #pragma unroll
                     for (int h = 0; h < 2; ++h)
@@ -855,35 +879,51 @@ __global__ void __launch_bounds__(AttCfg<D, NT>::T, 1) kv_attend_kernel(KvAttend
 #pragma unroll
                             for (int c = 0; c < 4; ++c) {
                                 const int t = t_first + 16 * h + 8 * (c >> 1) + r8, pos = qpos[nt][c & 1];
-                                if (t > pos || (a.window > 0 && t <= pos - a.window)) s[h][nt][c] = -INFINITY;
+                                if (t > pos || none || (a.window > 0 && t <= pos - a.window)) s[h][nt][c] = -INFINITY;
                             }
                 }
-                // The running maximum is moved when a score has passed it by more than the
-                // slack, the V scales' exponent when one has reached 2 with it.
+                // Weights are 2^(x - mo): at most 2^(10 - ve) when mo is set, and it is moved when one
+                // would pass 2^(14 - ve), so that weight times scale (below 2^(ve + 1)) fits fp16.
+                // (The weights are computed before it is known, again if it has to be moved.)
+                float w[2][NT][4];
+                auto weigh = [&] {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int c = 0; c < 4; ++c)
+                                w[h][nt][c] = ex2(fmaf(s[h][nt][c], q.f[nt][c & 1], -mo[nt][c & 1]));
+                };
+                weigh();
                 float tm[NT][2];
                 bool over = false;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
-                        tm[nt][c] = fmaxf(fmaxf(s[0][nt][c], s[0][nt][c + 2]), fmaxf(s[1][nt][c], s[1][nt][c + 2]));
-                        over |= tm[nt][c] > m[nt][c] + kAttSlack;
+                        tm[nt][c] = q.f[nt][c] *
+                                    fmaxf(fmaxf(s[0][nt][c], s[0][nt][c + 2]), fmaxf(s[1][nt][c], s[1][nt][c + 2]));
+                        over |= tm[nt][c] > mo[nt][c] + (float)(14 - ve);
                     }
-                const __half2 vmax = v_scale_max<D>(vpart, a.pg.vb, lane, hi_pos - t_first);
+                const __half2 vmax = v_scale_max<D>(vpart, a.pg.vb, lane, last);
                 const float vm = fmaxf(__low2float(vmax), __high2float(vmax));
-                const bool big = vm >= __uint_as_float((uint32_t)(128 + E2) << 23);
-                if (__any_sync(0xffffffffu, over || big)) {
+                over |= vm >= __uint_as_float((uint32_t)(128 + ve) << 23);
+                if (__any_sync(0xffffffffu, over)) {
+                    float t = vm;
+#pragma unroll
+                    for (int o = 1; o < 32; o <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, o));
+                    const int vn = min(max((int)(__float_as_uint(t) >> 23) - 127, ve), 15);
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                         for (int c = 0; c < 2; ++c) {
-                            float t = tm[nt][c];
+                            t = tm[nt][c];
 #pragma unroll
                             for (int o = 4; o < 32; o <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, o));
-                            const float mn = fmaxf(m[nt][c], t);
-                            const float k = m[nt][c] == mn ? 1.f : ex2(m[nt][c] - mn);
-                            m[nt][c] = mn;
-                            mo[nt][c] = (mn == -INFINITY ? 0.f : mn) - kAttShift;
+                            const float mn = fmaxf(mo[nt][c] + (float)(vn - ve), t - (float)(10 - vn));
+                            const float k = mo[nt][c] == mn ? 1.f : ex2(mo[nt][c] - mn);
+                            mo[nt][c] = mn;
                             l[nt][c] *= k;
 #pragma unroll
                             for (int i = 0; i < 2 * G; ++i) {
@@ -891,45 +931,28 @@ __global__ void __launch_bounds__(AttCfg<D, NT>::T, 1) kv_attend_kernel(KvAttend
                                 acc[nt][i][c + 2] *= k;
                             }
                         }
-                    if (__any_sync(0xffffffffu, big)) {
-                        float t = vm;
-#pragma unroll
-                        for (int o = 1; o < 32; o <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, o));
-                        const int en = min(max((int)(__float_as_uint(t) >> 23) - 127, E2), 15);
-                        const float k = __uint_as_float((uint32_t)(127 + E2 - en) << 23);
-                        E2 = en;
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                            for (int i = 0; i < 2 * G; ++i)
-#pragma unroll
-                                for (int c = 0; c < 4; ++c) acc[nt][i][c] *= k;
-                    }
+                    ve = vn;
+                    weigh();
                 }
                 uint32_t p[2][NT][2];
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
-                        const float p0 = ex2(s[h][nt][0] - mo[nt][0]), p1 = ex2(s[h][nt][1] - mo[nt][1]);
-                        const float p2 = ex2(s[h][nt][2] - mo[nt][0]), p3 = ex2(s[h][nt][3] - mo[nt][1]);
-                        l[nt][0] += p0 + p2;
-                        l[nt][1] += p1 + p3;
-                        p[h][nt][0] = movm_trans(h2_bits(__floats2half2_rn(p0, p1)));
-                        p[h][nt][1] = movm_trans(h2_bits(__floats2half2_rn(p2, p3)));
+                        l[nt][0] += w[h][nt][0] + w[h][nt][2];
+                        l[nt][1] += w[h][nt][1] + w[h][nt][3];
+                        p[h][nt][0] = movm_trans(h2_bits(__floats2half2_rn(w[h][nt][0], w[h][nt][1])));
+                        p[h][nt][1] = movm_trans(h2_bits(__floats2half2_rn(w[h][nt][2], w[h][nt][3])));
                     }
-                const __half2 es = __half2half2(__ushort_as_half((uint16_t)((15 - E2) << 10)));  // 2^-E2
-                // (15 - E2 is 0 for E2 = 15: the subnormal 2^-15)
-                const __half2 down = E2 == 15 ? bits_h2(0x02000200u) : es;
                 switch (a.pg.vb) {
 #define QG_OUTPUT(B)                                                   \
     case B:                                                            \
         if (masked) {                                                  \
-            output_half<D, NT, B, true>(vpart, 0, lane, down, p[0], acc);  \
-            output_half<D, NT, B, true>(vpart, 1, lane, down, p[1], acc);  \
+            output_half<D, NT, B, true>(vpart, 0, lane, p[0], acc);  \
+            output_half<D, NT, B, true>(vpart, 1, lane, p[1], acc);  \
         } else {                                                       \
-            output_half<D, NT, B, false>(vpart, 0, lane, down, p[0], acc); \
-            output_half<D, NT, B, false>(vpart, 1, lane, down, p[1], acc); \
+            output_half<D, NT, B, false>(vpart, 0, lane, p[0], acc); \
+            output_half<D, NT, B, false>(vpart, 1, lane, p[1], acc); \
         }                                                              \
         break;
                     QG_OUTPUT(2)
@@ -941,113 +964,123 @@ __global__ void __launch_bounds__(AttCfg<D, NT>::T, 1) kv_attend_kernel(KvAttend
 #undef QG_OUTPUT
                 }
             }
-            release();
-            if (flags & kDescLast) {
-                // this warp's part of the item is done: its slot, in the sums' own units
-                // (one that began before this warp is its first, and may leave copies in flight;
-                // one that goes on behind it is its last, and finds the ring drained)
-                float* slot = frag_head ? reinterpret_cast<float*>(rings + warp * a.ring_bytes) : slots + warp * C::SlotFloats;
-                AttFrag& fr = frags[warp * 2 + (frag_head ? 1 : 0)];
-                float unit[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    unit[i] = __uint_as_float((uint32_t)(127 + 24 + E2 - field_at(a.pg.vb, i)) << 23);
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-#pragma unroll
-                        for (int o = 4; o < 32; o <<= 1) l[nt][c] += __shfl_xor_sync(0xffffffffu, l[nt][c], o);
-                    }
-                if (frag_head && (flags & kDescTail)) {
-                    // the whole item: rotate back in this layout (dim 32 g + 4 r + i) and store
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int c = 0; c < 2; ++c) {
-                            float x[G][4];
-#pragma unroll
-                            for (int g = 0; g < G; ++g)
-#pragma unroll
-                                for (int i = 0; i < 4; ++i) x[g][i] = acc[nt][2 * g + (i >> 1)][(i & 1) * 2 + c] * unit[i];
-#pragma unroll
-                            for (int g = 0; g < G; ++g) {
-#pragma unroll
-                                for (int st = 1; st < 4; st <<= 1)
-#pragma unroll
-                                    for (int i = 0; i < 4; ++i)
-                                        if (!(i & st)) {
-                                            const float u = x[g][i], v = x[g][i + st];
-                                            x[g][i] = u + v;
-                                            x[g][i + st] = u - v;
-                                        }
-#pragma unroll
-                                for (int ls = 4; ls < 32; ls <<= 1)
-#pragma unroll
-                                    for (int i = 0; i < 4; ++i) {
-                                        const float o = __shfl_xor_sync(0xffffffffu, x[g][i], ls);
-                                        x[g][i] = (lane & ls) ? o - x[g][i] : x[g][i] + o;
-                                    }
-                            }
-#pragma unroll
-                            for (int st = 1; st < G; st <<= 1)
-#pragma unroll
-                                for (int g = 0; g < G; ++g)
-                                    if (!(g & st))
-#pragma unroll
-                                        for (int i = 0; i < 4; ++i) {
-                                            const float u = x[g][i], v = x[g + st][i];
-                                            x[g][i] = u + v;
-                                            x[g + st][i] = u - v;
-                                        }
-                            const int r = d.z * RB + 8 * nt + 2 * j + c;
-                            if (r < cs.n * a.group) {
-                                const int tok = r / a.group, hq = head * a.group + (r - tok * a.group);
-                                const float inv = l[nt][c] == 0.f ? 0.f : 1.f / (l[nt][c] * (float)D);
-                                uint16_t* o = reinterpret_cast<uint16_t*>(a.out.p) + (cs.row0 + tok) * a.out.row +
-                                              hq * a.out.head + 4 * r8;
-#pragma unroll
-                                for (int g = 0; g < G; ++g) {
-                                    uint16_t v[4];
-#pragma unroll
-                                    for (int i = 0; i < 4; ++i) v[i] = kv_from_float<BF16>(x[g][i] * inv);
-                                    *reinterpret_cast<uint2*>(o + 32 * g) =
-                                        make_uint2(v[0] | (uint32_t)v[1] << 16, v[2] | (uint32_t)v[3] << 16);
-                                }
-                                if (a.lse && r8 == 0)
-                                    a.lse[(int64_t)(cs.row0 + tok) * a.q_heads + hq] =
-                                        (m[nt][c] + log2f(l[nt][c]) - kAttShift) * 0.6931471805599453f;
-                            }
-                        }
-                } else {
-                    __syncwarp();
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int c = 0; c < 2; ++c) {
-                            const int r = 8 * nt + 2 * j + c;
-#pragma unroll
-                            for (int g = 0; g < G; ++g)
-                                *reinterpret_cast<float4*>(slot + r * C::OS + 32 * g + 4 * r8) =
-                                    make_float4(acc[nt][2 * g][c] * unit[0], acc[nt][2 * g][c + 2] * unit[1],
-                                                acc[nt][2 * g + 1][c] * unit[2], acc[nt][2 * g + 1][c + 2] * unit[3]);
-                            if (r8 == 0) {
-                                slot[RB * C::OS + r] = m[nt][c];
-                                slot[RB * C::OS + RB + r] = l[nt][c];
-                            }
-                        }
-                    if (lane == 0) {
-                        // the item's first tile as a number of the call: this tile's less its place
-                        fr.item = w0 + done - d.w;
-                        fr.seq = d.x;
-                        fr.head = head;
-                        fr.rb = d.z;
-                        fr.tiles = cs.tiles;
-                    }
-                }
+            __syncwarp();
+            if (left > 0) issue(stage);
+            if (++stage == a.stages) {
+                stage = 0;
+                parity ^= 1;
             }
         }
+        // this warp's part of the item is done: its slot, in the sums' own units
+        const bool frag_head = cc.tile == 0;
+        // (one that began before this warp is its first, and may leave copies in flight;
+        // one that goes on behind it is its last, and finds the ring drained)
+        float* slot = frag_head ? reinterpret_cast<float*>(ring) : slots + warp * C::SlotFloats;
+        AttFrag& fr = frags[warp * 2 + (frag_head ? 1 : 0)];
+        float unit[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            unit[i] = __uint_as_float((uint32_t)(127 + 24 - field_at(a.pg.vb, i)) << 23);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1) l[nt][c] += __shfl_xor_sync(0xffffffffu, l[nt][c], o);
+            }
+        if (frag_head && cc.tile + n_tiles == cs.tiles) {
+            // the whole item: rotate back in this layout (dim 32 g + 4 r + i) and store
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    float x[G][4];
+#pragma unroll
+                    for (int g = 0; g < G; ++g)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) x[g][i] = acc[nt][2 * g + (i >> 1)][(i & 1) * 2 + c] * unit[i];
+#pragma unroll
+                    for (int g = 0; g < G; ++g) {
+#pragma unroll
+                        for (int st = 1; st < 4; st <<= 1)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                if (!(i & st)) {
+                                    const float u = x[g][i], v = x[g][i + st];
+                                    x[g][i] = u + v;
+                                    x[g][i + st] = u - v;
+                                }
+#pragma unroll
+                        for (int ls = 4; ls < 32; ls <<= 1)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const float o = __shfl_xor_sync(0xffffffffu, x[g][i], ls);
+                                x[g][i] = (lane & ls) ? o - x[g][i] : x[g][i] + o;
+                            }
+                    }
+#pragma unroll
+                    for (int st = 1; st < G; st <<= 1)
+#pragma unroll
+                        for (int g = 0; g < G; ++g)
+                            if (!(g & st))
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) {
+                                    const float u = x[g][i], v = x[g + st][i];
+                                    x[g][i] = u + v;
+                                    x[g + st][i] = u - v;
+                                }
+                    const int r = r_base + 8 * nt + 2 * j + c;
+                    if (r < rows) {
+                        const int tok = r / a.group, hq = cc.h * a.group + (r - tok * a.group);
+                        const float inv = l[nt][c] == 0.f ? 0.f : 1.f / (l[nt][c] * (float)D);
+                        uint16_t* o = reinterpret_cast<uint16_t*>(a.out.p) + (cs.row0 + tok) * a.out.row +
+                                      hq * a.out.head + 4 * r8;
+#pragma unroll
+                        for (int g = 0; g < G; ++g) {
+                            uint16_t v[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) v[i] = kv_from_float<BF16>(x[g][i] * inv);
+                            *reinterpret_cast<uint2*>(o + 32 * g) =
+                                make_uint2(v[0] | (uint32_t)v[1] << 16, v[2] | (uint32_t)v[3] << 16);
+                        }
+                        if (a.lse && r8 == 0)
+                            a.lse[(int64_t)(cs.row0 + tok) * a.q_heads + hq] =
+                                (mo[nt][c] + log2f(l[nt][c])) * 0.6931471805599453f;
+                    }
+                }
+        } else {
+            __syncwarp();
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const int r = 8 * nt + 2 * j + c;
+#pragma unroll
+                    for (int g = 0; g < G; ++g)
+                        *reinterpret_cast<float4*>(slot + r * C::OS + 32 * g + 4 * r8) =
+                            make_float4(acc[nt][2 * g][c] * unit[0], acc[nt][2 * g][c + 2] * unit[1],
+                                        acc[nt][2 * g + 1][c] * unit[2], acc[nt][2 * g + 1][c + 2] * unit[3]);
+                    if (r8 == 0) {
+                        slot[RB * C::OS + r] = mo[nt][c];
+                        slot[RB * C::OS + RB + r] = l[nt][c];
+                    }
+                }
+            if (lane == 0) {
+                // the item's first tile as a number of the call
+                fr.item = at - cc.tile;
+                fr.seq = cc.b;
+                fr.head = cc.h;
+                fr.rb = cc.rb;
+                fr.tiles = cs.tiles;
+            }
+        }
+        at += n_tiles;
+        count -= n_tiles;
+        cc.tile = cs.tiles - 1;
+        att_next<RB>(a, cc, count > 0);
     }
+    if (dead)  // what is still in flight into this warp's ring
+        for (int i = 0; i < a.stages; ++i) mbar_wait(&full[i], parity ^ (i < stage ? 1 : 0));
     __syncthreads();
 
     // ---- join: fragments lie in order (warp, slot); those of one item are neighbours
@@ -1070,7 +1103,7 @@ __global__ void __launch_bounds__(AttCfg<D, NT>::T, 1) kv_attend_kernel(KvAttend
     const uint32_t upto = heads & ((2u << lane) - 1u), above = heads & ~((2u << lane) - 1u);
     const int gfirst = upto ? 31 - __clz(upto) : 0, gend = above ? __ffs(above) - 1 : 2 * W;
     const bool whole = fr.item >= cta0 && fr.item + fr.tiles <= cta1;
-    for (int r = warp; r < RB; r += W + 1) {
+    for (int r = warp; r < RB; r += W) {
         const float* sl = slot_of(active ? lane : gfirst);
         const float ms = active ? sl[RB * C::OS + r] : -INFINITY, ls = active ? sl[RB * C::OS + RB + r] : 0.f;
         float mx = ms;
@@ -1135,7 +1168,7 @@ __global__ void __launch_bounds__(AttCfg<D, NT>::T, 1) kv_attend_kernel(KvAttend
         __threadfence();
         sh_last[fr.item < cta0 ? 0 : 1] = last;
     }
-    for (int i = warp; i < __popc(wholes) * RB; i += W + 1) {
+    for (int i = warp; i < __popc(wholes) * RB; i += W) {
         const int f = __fns(wholes, 0, i / RB + 1), r = i % RB;
         const AttFrag& g = frags[f];
         const AttSeq s = att_seq<RB>(a, g.seq);
@@ -1154,7 +1187,7 @@ __global__ void __launch_bounds__(AttCfg<D, NT>::T, 1) kv_attend_kernel(KvAttend
         const AttSeq s = att_seq<RB>(a, g.seq);
         auto part_of = [&](int k) { return a.partial + ((size_t)k * 2 + (k == c0 ? 1 : 0)) * C::GSlot; };
         __syncthreads();
-        for (int r = warp; r < RB; r += W + 1) {
+        for (int r = warp; r < RB; r += W) {
             float ms[C::MaxCtas / 32], mx = -INFINITY, lt = 0.f;
 #pragma unroll
             for (int i = 0; i < C::MaxCtas / 32; ++i) {
@@ -1195,7 +1228,7 @@ __global__ void __launch_bounds__(AttCfg<D, NT>::T, 1) kv_attend_kernel(KvAttend
             *reinterpret_cast<float4*>(rowbuf + 4 * i) = o;
         }
         __syncthreads();
-        for (int r = warp; r < min(RB, s.n * a.group - g.rb * RB); r += W + 1) {
+        for (int r = warp; r < min(RB, s.n * a.group - g.rb * RB); r += W) {
             float o[E];
 #pragma unroll
             for (int k = 0; k < E; ++k) o[k] = rowbuf[r * D + E * lane + k];

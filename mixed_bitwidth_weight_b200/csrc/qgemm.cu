@@ -957,11 +957,10 @@ template <int D, int NT, bool BF16>
 int launch_attend(KvAttend a, DeviceInfo* dev, bool* attr, cudaStream_t s) {
     using C = AttCfg<D, NT>;
     constexpr size_t most = 226 * 1024;  // 227 KB a CTA, some of it static
-    // a stage holds the K or the V part of a record; the ring also takes a fragment at the end
-    const size_t part = (size_t)4 * D * std::max(a.pg.kb, a.pg.vb) + 2 * D, room = (most - C::RingAt) / C::W / 128 * 128;
-    a.stages = (int)std::min<size_t>(kAttMaxStages, room / part);
-    a.stage_bytes = (int)part;
-    a.ring_bytes = (int)(std::max(a.stages * part, (size_t)C::SlotBytes) + 127) / 128 * 128;
+    // the ring's stages are whole records; at the end it also takes a fragment
+    const size_t rec = (size_t)4 * D * (a.pg.kb + a.pg.vb + 1), room = (most - C::RingAt) / C::W / 128 * 128;
+    a.stages = (int)std::min<size_t>(kAttMaxStages, room / rec);
+    a.ring_bytes = (int)((std::max(a.stages * rec, (size_t)C::SlotBytes) + 127) / 128 * 128);
     if (a.stages < 1 || (size_t)a.ring_bytes > room) return QGEMM_ERR_UNSUPPORTED;
     if (!*attr) {  // a per-device setting
         if (cudaFuncSetAttribute(kv_attend_kernel<D, NT, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
