@@ -57,7 +57,7 @@ constexpr float kAttNone = -3.4e38f;  // the weights' offset before any token: b
 
 template <int D, int NT>
 struct AttCfg {
-    static constexpr int W = D * NT <= 128 ? 11 : 7;  // warps: 168 registers a thread with 11, 255 with 7
+    static constexpr int W = D * NT <= 128 ? 8 : 7;  // warps: 255 registers a thread
     static constexpr int T = 32 * W;
     static constexpr int G = D / 32;
     static constexpr int RB = 8 * NT;                 // query rows of an item
@@ -128,18 +128,28 @@ QG_DEV __half2 bits_h2(uint32_t u) { return *reinterpret_cast<__half2*>(&u); }
 // Fields of one 32-bit word: its low half holds n codes of one row, its high
 // half the n codes that pair with them (n = 4 for b <= 4, else 2).  Field i is
 // used where it lies when it ends below bit 10 (a subnormal's mantissa), else
-// the word is shifted down first.
+// the word is shifted down first.  At 4 bits the odd fields keep the code below
+// them, c_i + 16 c_{i+1}, which saves a shift per word: the query's even entries
+// take q_i - q_{i+1} / 16 for it, and the output's odd rows (O_i + 16 O_{i+1})
+// are parted at the end, both linear.
 template <int B>
 struct Fld {
     static constexpr int N = B <= 4 ? 4 : 2;
     static constexpr int pre(int i) { return B * i + B <= 10 ? 0 : (B == 4 ? 8 : B * i); }
     static constexpr int at(int i) { return B * i - pre(i); }  // the value is c 2^(at - 24)
-    static constexpr uint32_t mask(int i) { return (((1u << B) - 1u) << at(i)) * 0x10001u; }
-    static constexpr uint32_t zero(int i) { return ((1u << (B - 1)) << at(i)) * 0x10001u; }
+    static constexpr uint32_t mask(int i) {
+        return (B == 4 && (i & 1) ? 0xffu : ((1u << B) - 1u) << at(i)) * 0x10001u;
+    }
+    static constexpr uint32_t zero(int i) {
+        return (B == 4 && (i & 1) ? 0x88u : (1u << (B - 1)) << at(i)) * 0x10001u;
+    }
 };
 
 template <int B, int I>
 QG_DEV uint32_t field(uint32_t x) {
+    if constexpr (B == 4 && I == 3) return __byte_perm(x, 0, 0x4341);  // the upper byte of each half
+    if constexpr (B == 4 && I == 2) return __byte_perm(x, 0, 0x4341) & Fld<B>::mask(I);
+    if constexpr (B == 8 && I == 1) return __byte_perm(x, 0, 0x4341);
     if constexpr (Fld<B>::pre(I) == 0) return x & Fld<B>::mask(I);
     return (x >> Fld<B>::pre(I)) & Fld<B>::mask(I);
 }
@@ -229,6 +239,14 @@ struct AttQ {
     uint32_t hi[NT][D / 32][4], lo[NT][D / 32][4];
     float zq[NT][D / 32][4];  // an accumulator's four: rows r and r + 8 start alike
     float f[NT][2];  // factor of a score, log2 units
+    // the accumulators' C operand is four consecutive registers: without the moves that the compiler
+    // cannot see through it keeps two and copies them before each use
+    QG_DEV void set_zero(int nt, int g, float x, float y) {
+        zq[nt][g][0] = x;
+        zq[nt][g][1] = y;
+        asm volatile("mov.b32 %0, %1;" : "=f"(zq[nt][g][2]) : "f"(x));
+        asm volatile("mov.b32 %0, %1;" : "=f"(zq[nt][g][3]) : "f"(y));
+    }
 };
 
 // A registers of one k step (0, 1) of group g: rows tokens 8 tt + r (word x0's) and 8 (tt + 1) + r (x1's)
@@ -376,7 +394,9 @@ QG_DEV void rotate_query(const KvAttend& a, const uint16_t* p, float* area, int 
 #pragma unroll
     for (int i = 0; i < E; ++i) {
         const int d = E * lane + i, pair = d & 3;
-        const float v = x[i] * rs.up, vd = v * __uint_as_float((uint32_t)(127 - field_at(a.pg.kb, pair)) << 23);
+        const float v = x[i] * rs.up;
+        float vd = v * __uint_as_float((uint32_t)(127 - field_at(a.pg.kb, pair)) << 23);
+        if (a.pg.kb == 4 && !(i & 1)) vd = fmaf(x[(i + 1) % E] * rs.up, -0.0625f, vd);
         const __half hi = __float2half_rn(vd), lo = __float2half_rn(vd - __half2float(hi));
         const int at = ((((nt * G + g) * 2) * 32 + 4 * n + ((d & 31) >> 3)) * 4 + pair) * 2 + ((d >> 2) & 1);
         out[at] = __half_as_ushort(hi);
@@ -452,16 +472,20 @@ QG_DEV void rotate_queries(const KvAttend& a, int row0, int rows, int r_base, in
             for (int i = 0; i < 4; ++i) {
                 const float u = x[g][i] * rs.up, v = x[g][i + 4] * rs.up;
                 const float dn = __uint_as_float((uint32_t)(127 - field_at(a.pg.kb, i)) << 23);
-                const __half2 hi = __floats2half2_rn(u * dn, v * dn);
+                float ud = u * dn, vd = v * dn;
+                if (a.pg.kb == 4 && !(i & 1)) {
+                    ud = fmaf(x[g][(i + 1) & 3] * rs.up, -0.0625f, ud);
+                    vd = fmaf(x[g][4 + ((i + 1) & 3)] * rs.up, -0.0625f, vd);
+                }
+                const __half2 hi = __floats2half2_rn(ud, vd);
                 q.hi[nt][g][i] = h2_bits(hi);
-                q.lo[nt][g][i] = h2_bits(__floats2half2_rn(u * dn - __low2float(hi), v * dn - __high2float(hi)));
+                q.lo[nt][g][i] = h2_bits(__floats2half2_rn(ud - __low2float(hi), vd - __high2float(hi)));
                 sum += u + v;
             }
             sum += __shfl_xor_sync(0xffffffffu, sum, 1);
             sum += __shfl_xor_sync(0xffffffffu, sum, 2);
             sum *= rs.zero;
-            q.zq[nt][g][0] = q.zq[nt][g][2] = __shfl_sync(0xffffffffu, sum, src);
-            q.zq[nt][g][1] = q.zq[nt][g][3] = __shfl_sync(0xffffffffu, sum, src + 4);
+            q.set_zero(nt, g, __shfl_sync(0xffffffffu, sum, src), __shfl_sync(0xffffffffu, sum, src + 4));
         }
         q.f[nt][0] = __shfl_sync(0xffffffffu, rs.f, src);
         q.f[nt][1] = __shfl_sync(0xffffffffu, rs.f, src + 4);
@@ -481,8 +505,7 @@ QG_DEV void load_queries(const float* area, int lane, AttQ<D, NT>& q) {
             q.hi[nt][g][0] = h.x, q.hi[nt][g][1] = h.y, q.hi[nt][g][2] = h.z, q.hi[nt][g][3] = h.w;
             q.lo[nt][g][0] = l.x, q.lo[nt][g][1] = l.y, q.lo[nt][g][2] = l.z, q.lo[nt][g][3] = l.w;
             const float2 z = *reinterpret_cast<const float2*>(area + C::QZero + (nt * G + g) * 8 + 2 * (lane & 3));
-            q.zq[nt][g][0] = q.zq[nt][g][2] = z.x;
-            q.zq[nt][g][1] = q.zq[nt][g][3] = z.y;
+            q.set_zero(nt, g, z.x, z.y);
         }
         const float2 v = *reinterpret_cast<const float2*>(area + C::QFactor + nt * 8 + 2 * (lane & 3));
         q.f[nt][0] = v.x;
@@ -769,35 +792,43 @@ __global__ void __launch_bounds__(AttCfg<D, NT>::T, 1) kv_attend_kernel(KvAttend
     // ---- The ring: whole records, each warp its own.
     const int lps = 31 - __clz(a.pg.page_size / kTileTokens);  // log2 tiles per page
     int page_base = 0, page_b = -1, page_id = 0;               // lane i: page page_base + i of sequence page_b
-    int left = count;
-    uint32_t bad = 0;  // stages whose tile has no page
-    bool dead = false;
+    int left = count, page_left = 0;                           // tiles of the run, of the page, still to copy
+    uint32_t bad = 0;                                          // stages whose tile has no page
+    bool dead = false, has = false;
+    const uint8_t* src = nullptr;
     auto issue = [&](int s) {
-        const int t = pc.s.t0 + pc.tile, pi = t >> lps;
-        if (page_b != pc.b || (uint32_t)(pi - page_base) >= 32u) {
-            page_b = pc.b;
-            page_base = pi;
-            const int i = pi + lane;
-            page_id = i < a.bt.max_pages && ((int64_t)i << lps) * kTileTokens < pc.s.len
-                          ? a.bt.table[pc.b * a.bt.table_stride + i]
-                          : -1;
+        if (page_left == 0) {
+            const int t = pc.s.t0 + pc.tile, pi = t >> lps, in = t & ((1 << lps) - 1);
+            if (page_b != pc.b || (uint32_t)(pi - page_base) >= 32u) {
+                page_b = pc.b;
+                page_base = pi;
+                const int i = pi + lane;
+                page_id = i < a.bt.max_pages && ((int64_t)i << lps) * kTileTokens < pc.s.len
+                              ? a.bt.table[pc.b * a.bt.table_stride + i]
+                              : -1;
+            }
+            const int page = __shfl_sync(0xffffffffu, page_id, pi - page_base);
+            has = (uint32_t)page < (uint32_t)a.pg.num_pages && pc.s.len > 0;
+            if (!has && pc.s.len > 0 && lane == 0) set_dev_error(QGEMM_DEV_BAD_PAGE);
+            src = a.pg.base + page * a.pg.page_bytes + (int64_t)((pc.h << lps) + in) * rec_bytes;
+            page_left = min((1 << lps) - in, pc.s.tiles - pc.tile);
         }
-        const int page = __shfl_sync(0xffffffffu, page_id, pi - page_base);
-        const bool has = (uint32_t)page < (uint32_t)a.pg.num_pages && pc.s.len > 0;
-        bad = has ? bad & ~(1u << s) : bad | 1u << s;
+        bad = (bad & ~(1u << s)) | (has ? 0u : 1u << s);
         if (lane == 0) {
             if (has && !dead) {
-                const uint8_t* src = a.pg.base + page * a.pg.page_bytes +
-                                     (int64_t)((pc.h << lps) + (t & ((1 << lps) - 1))) * rec_bytes;
                 mbar_arrive_expect_tx(&full[s], rec_bytes);
                 bulk_g2s(ring + s * rec_bytes, src, rec_bytes, &full[s]);
             } else {
-                if (!has && pc.s.len > 0) set_dev_error(QGEMM_DEV_BAD_PAGE);
                 mbar_arrive(&full[s]);
             }
         }
+        src += rec_bytes;
         --left;
-        att_next<RB>(a, pc, left > 0);
+        ++pc.tile;
+        if (--page_left == 0 && pc.tile == pc.s.tiles) {
+            --pc.tile;
+            att_next<RB>(a, pc, left > 0);
+        }
     };
     for (int i = 0; i < a.stages && left > 0; ++i) issue(i);
 
@@ -813,7 +844,7 @@ __global__ void __launch_bounds__(AttCfg<D, NT>::T, 1) kv_attend_kernel(KvAttend
     // ---- one warp's run, item by item
     AttQ<D, NT> q;
     float acc[NT][2 * G][4], mo[NT][2], l[NT][2];  // weights are 2^(x - mo)
-    int stage = 0, parity = 0;
+    int stage = 0, parity = 0, rec_at = 0;
     const int j = lane & 3, r8 = lane >> 2;
     for (long long at = w0; count > 0;) {
         const AttSeq& cs = cc.s;
@@ -826,13 +857,17 @@ __global__ void __launch_bounds__(AttCfg<D, NT>::T, 1) kv_attend_kernel(KvAttend
         ++my_item;
         const int lo_pos = cs.pos0 + r_base / a.group;
         const int hi_pos = cs.pos0 + (min(r_base + RB, rows) - 1) / a.group;
+        // tiles [u0, u1) of these are seen whole by every row
+        const int t_base = (cs.t0 + cc.tile) * kTileTokens;
+        const int u1 = (lo_pos + 1 - t_base) >> 5, u0 = a.window > 0 ? ((hi_pos - a.window - t_base) >> 5) + 1 : 0;
         int qpos[NT][2], ve = 0;  // ve: exponent of the largest V scale, 0 at least
+        float limit[NT][2];       // a score may reach this before mo moves
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 qpos[nt][c] = cs.pos0 + (r_base + 8 * nt + 2 * j + c) / a.group;
-                mo[nt][c] = kAttNone;
+                mo[nt][c] = limit[nt][c] = kAttNone;
                 l[nt][c] = 0.f;
             }
 #pragma unroll
@@ -847,9 +882,8 @@ __global__ void __launch_bounds__(AttCfg<D, NT>::T, 1) kv_attend_kernel(KvAttend
             // (given up: no copy is issued any more and nothing is waited for; the run goes on over
             // whatever the ring holds, and the error word says so)
             float s[2][NT][4];
-            const uint8_t* rec = ring + stage * rec_bytes;
+            const uint8_t* rec = ring + rec_at;
             const uint8_t* vpart = rec + k_bytes;
-            const int t_first = (cs.t0 + cc.tile + it) * kTileTokens;
             {
                 switch (a.pg.kb) {
 #define QG_SCORES(B)                            \
@@ -868,10 +902,11 @@ __global__ void __launch_bounds__(AttCfg<D, NT>::T, 1) kv_attend_kernel(KvAttend
             {
                 // a tile without a page shows nothing
                 const bool none = bad >> stage & 1;
-                const bool masked = t_first + kTileTokens - 1 > lo_pos || none ||
-                                    (a.window > 0 && t_first <= hi_pos - a.window);
-                const int last = none ? -1 : hi_pos - t_first;  // last slot that any row sees
+                const bool masked = it < u0 || it >= u1 || none;
+                int last = kTileTokens;  // last slot that any row sees
                 if (masked) {
+                    const int t_first = t_base + it * kTileTokens;
+                    last = none ? -1 : hi_pos - t_first;
 #pragma unroll
                     for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -904,13 +939,12 @@ __global__ void __launch_bounds__(AttCfg<D, NT>::T, 1) kv_attend_kernel(KvAttend
                     for (int c = 0; c < 2; ++c) {
                         tm[nt][c] = q.f[nt][c] *
                                     fmaxf(fmaxf(s[0][nt][c], s[0][nt][c + 2]), fmaxf(s[1][nt][c], s[1][nt][c + 2]));
-                        over |= tm[nt][c] > mo[nt][c] + (float)(14 - ve);
+                        over |= tm[nt][c] > limit[nt][c];
                     }
                 const __half2 vmax = v_scale_max<D>(vpart, a.pg.vb, lane, last);
-                const float vm = fmaxf(__low2float(vmax), __high2float(vmax));
-                over |= vm >= __uint_as_float((uint32_t)(128 + ve) << 23);
+                over |= !__hblt2(vmax, bits_h2((uint32_t)(16 + ve) * 0x04000400u));  // 2^(ve + 1), infinity for 15
                 if (__any_sync(0xffffffffu, over)) {
-                    float t = vm;
+                    float t = fmaxf(__low2float(vmax), __high2float(vmax));
 #pragma unroll
                     for (int o = 1; o < 32; o <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, o));
                     const int vn = min(max((int)(__float_as_uint(t) >> 23) - 127, ve), 15);
@@ -924,6 +958,7 @@ __global__ void __launch_bounds__(AttCfg<D, NT>::T, 1) kv_attend_kernel(KvAttend
                             const float mn = fmaxf(mo[nt][c] + (float)(vn - ve), t - (float)(10 - vn));
                             const float k = mo[nt][c] == mn ? 1.f : ex2(mo[nt][c] - mn);
                             mo[nt][c] = mn;
+                            limit[nt][c] = mn + (float)(14 - vn);
                             l[nt][c] *= k;
 #pragma unroll
                             for (int i = 0; i < 2 * G; ++i) {
@@ -966,8 +1001,9 @@ __global__ void __launch_bounds__(AttCfg<D, NT>::T, 1) kv_attend_kernel(KvAttend
             }
             __syncwarp();
             if (left > 0) issue(stage);
+            rec_at += rec_bytes;
             if (++stage == a.stages) {
-                stage = 0;
+                stage = rec_at = 0;
                 parity ^= 1;
             }
         }
@@ -977,10 +1013,17 @@ __global__ void __launch_bounds__(AttCfg<D, NT>::T, 1) kv_attend_kernel(KvAttend
         // one that goes on behind it is its last, and finds the ring drained)
         float* slot = frag_head ? reinterpret_cast<float*>(ring) : slots + warp * C::SlotFloats;
         AttFrag& fr = frags[warp * 2 + (frag_head ? 1 : 0)];
-        float unit[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            unit[i] = __uint_as_float((uint32_t)(127 + 24 - field_at(a.pg.vb, i)) << 23);
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 2 * G; ++i)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    float &u = acc[nt][i][c], &v = acc[nt][i][c + 2];  // fields 2 (i % 2) and the next
+                    u *= __uint_as_float((uint32_t)(127 + 24 - field_at(a.pg.vb, 2 * (i & 1))) << 23);
+                    v *= __uint_as_float((uint32_t)(127 + 24 - field_at(a.pg.vb, 2 * (i & 1) + 1)) << 23);
+                    if (a.pg.vb == 4) v -= u * 0.0625f;
+                }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -998,7 +1041,7 @@ __global__ void __launch_bounds__(AttCfg<D, NT>::T, 1) kv_attend_kernel(KvAttend
 #pragma unroll
                     for (int g = 0; g < G; ++g)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) x[g][i] = acc[nt][2 * g + (i >> 1)][(i & 1) * 2 + c] * unit[i];
+                        for (int i = 0; i < 4; ++i) x[g][i] = acc[nt][2 * g + (i >> 1)][(i & 1) * 2 + c];
 #pragma unroll
                     for (int g = 0; g < G; ++g) {
 #pragma unroll
@@ -1058,8 +1101,8 @@ __global__ void __launch_bounds__(AttCfg<D, NT>::T, 1) kv_attend_kernel(KvAttend
 #pragma unroll
                     for (int g = 0; g < G; ++g)
                         *reinterpret_cast<float4*>(slot + r * C::OS + 32 * g + 4 * r8) =
-                            make_float4(acc[nt][2 * g][c] * unit[0], acc[nt][2 * g][c + 2] * unit[1],
-                                        acc[nt][2 * g + 1][c] * unit[2], acc[nt][2 * g + 1][c + 2] * unit[3]);
+                            make_float4(acc[nt][2 * g][c], acc[nt][2 * g][c + 2], acc[nt][2 * g + 1][c],
+                                        acc[nt][2 * g + 1][c + 2]);
                     if (r8 == 0) {
                         slot[RB * C::OS + r] = mo[nt][c];
                         slot[RB * C::OS + RB + r] = l[nt][c];
