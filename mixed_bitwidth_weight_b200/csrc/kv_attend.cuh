@@ -45,7 +45,7 @@ struct KvAttend {
     KvBatch bt;
     KvRows q, out;
     float* lse;  // [rows][q_heads] or null
-    int32_t q_heads, group, window;
+    int32_t q_heads, group, window, bf16;
     int32_t stages, ring_bytes;  // of a warp's ring
     float scale;
     unsigned int* tickets;  // [CTAs], zero between calls
@@ -280,7 +280,7 @@ QG_DEV void k_fragment(const uint32_t (&w)[D * B / 64], int g, int step, uint32_
 // with 64 dims) hide each other's latency.
 template <int D, int NT, int B>
 QG_DEV void scores_tile(const uint8_t* rec, int lane, const AttQ<D, NT>& q, float (&s)[2][NT][4]) {
-    constexpr int G = D / 32, NW = D * B / 64, HB = 1;  // halves at a time
+    constexpr int G = D / 32, NW = D * B / 64, HB = D * NT > 128 ? 1 : 2;  // halves at a time
 #pragma unroll
     for (int h0 = 0; h0 < 2; h0 += HB) {
         uint32_t w[HB][NW], sc[HB][G];
@@ -350,6 +350,10 @@ QG_DEV void scores_tile(const uint8_t* rec, int lane, const AttQ<D, NT>& q, floa
     }
 }
 
+// a value of the call's type, fp16 or bf16
+QG_DEV float att_in(const KvAttend& a, uint16_t v) { return a.bf16 ? kv_to_float<true>(v) : kv_to_float<false>(v); }
+QG_DEV uint16_t att_out(const KvAttend& a, float v) { return a.bf16 ? kv_from_float<true>(v) : kv_from_float<false>(v); }
+
 // A rotated row's power-of-two scale (largest magnitude into [2^14, 2^15), so that
 // both fp16 parts keep their bits; the score scale's sign goes with it), -z 2^-24,
 // and the factor that turns a score into log2 units.  The factor is positive, so
@@ -374,13 +378,13 @@ QG_DEV AttRowScale att_row_scale(const KvAttend& a, float amax) {
 // Rotate query row n (of 8) of row tile nt, a warp to a row, split it into its two
 // parts and put them where the B operand's lanes read them (row n's dims
 // 32 g + 8 j + i are lane 4 n + j's, pair i % 4, half i / 4).  p: the row in shared memory.
-template <int D, int NT, bool BF16>
+template <int D, int NT>
 QG_DEV void rotate_query(const KvAttend& a, const uint16_t* p, float* area, int nt, int n, int lane) {
     using C = AttCfg<D, NT>;
     constexpr int E = D / 32, G = D / 32;
     float x[E];
 #pragma unroll
-    for (int i = 0; i < E; ++i) x[i] = kv_to_float<BF16>(p[E * lane + i]);
+    for (int i = 0; i < E; ++i) x[i] = att_in(a, p[E * lane + i]);
     fwht_warp<E>(x, lane);
     float amax = 0.f;
 #pragma unroll
@@ -412,7 +416,7 @@ QG_DEV void rotate_query(const KvAttend& a, const uint16_t* p, float* area, int 
 // The same for all rows of an item by one warp for itself, straight into the B
 // operand's registers: lane 4 n + j rotates its share of row n, strides 1, 2, 4 and
 // 32 .. within the lane, 8 and 16 between the four lanes of the row.
-template <int D, int NT, bool BF16>
+template <int D, int NT>
 QG_DEV void rotate_queries(const KvAttend& a, int row0, int rows, int r_base, int head, int lane, AttQ<D, NT>& q) {
     constexpr int G = D / 32;
 #pragma unroll
@@ -432,7 +436,7 @@ QG_DEV void rotate_queries(const KvAttend& a, int row0, int rows, int r_base, in
                 const uint32_t v[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                    x[g][i] = kv_to_float<BF16>((uint16_t)((i & 1) ? v[i / 2] >> 16 : v[i / 2] & 0xffff));
+                    x[g][i] = att_in(a, (uint16_t)((i & 1) ? v[i / 2] >> 16 : v[i / 2] & 0xffff));
             }
         }
         float amax = 0.f;
@@ -523,56 +527,53 @@ QG_DEV void output_half(const uint8_t* part, int half, int lane, const uint32_t 
     uint32_t w[NW];
     load_words<D, B>(part, half, lane, w);
     const uint8_t* scales = part + 4 * D * B + ((lane & 3) * G * 8 + 4 * half) * 2;
-    constexpr int GB = 1;
 #pragma unroll
-    for (int g0 = 0; g0 < G; g0 += GB) {
-        uint32_t b0[GB][NT], b1[GB][NT];
+    for (int g = 0; g < G; ++g) {
+        const uint2 su = *reinterpret_cast<const uint2*>(scales + g * 16);
+        uint32_t b0[NT], b1[NT];
 #pragma unroll
-        for (int gi = 0; gi < GB; ++gi) {
-            const int g = g0 + gi;
-            const uint2 su = *reinterpret_cast<const uint2*>(scales + g * 16);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                b0[gi][nt] = h2_bits(__hmul2(bits_h2(p[nt][0]), bits_h2(su.x)));
-                b1[gi][nt] = h2_bits(__hmul2(bits_h2(p[nt][1]), bits_h2(su.y)));
-                if constexpr (Masked) {  // a weight of 0 is 0 whatever the scale it meets
-                    b0[gi][nt] &= __hneu2_mask(bits_h2(p[nt][0]), bits_h2(0));
-                    b1[gi][nt] &= __hneu2_mask(bits_h2(p[nt][1]), bits_h2(0));
-                }
+        for (int nt = 0; nt < NT; ++nt) {
+            b0[nt] = h2_bits(__hmul2(bits_h2(p[nt][0]), bits_h2(su.x)));
+            b1[nt] = h2_bits(__hmul2(bits_h2(p[nt][1]), bits_h2(su.y)));
+            if constexpr (Masked) {  // a weight of 0 is 0 whatever the scale it meets
+                b0[nt] &= __hneu2_mask(bits_h2(p[nt][0]), bits_h2(0));
+                b1[nt] &= __hneu2_mask(bits_h2(p[nt][1]), bits_h2(0));
             }
         }
+        const int unit = (g >> 1) * 8 * B + (g & 1) * 4 * B;  // this group's four codes in a token's units
+        uint32_t f[2][4];
 #pragma unroll
-        for (int gi = 0; gi < GB; ++gi) {
-            const int g = g0 + gi;
-            const int unit = (g >> 1) * 8 * B + (g & 1) * 4 * B;  // this group's four codes in a token's units
-            uint32_t f[2][4];
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const int t0 = (2 * k) * UT + unit, t1 = (2 * k + 1) * UT + unit;
-                if constexpr (B <= 4) {
-                    const uint32_t x = halves_from(w, t0, t1, 4 * B);
-                    f[k][0] = field<B, 0>(x);
-                    f[k][1] = field<B, 1>(x);
-                    f[k][2] = field<B, 2 % Fld<B>::N>(x);
-                    f[k][3] = field<B, 3 % Fld<B>::N>(x);
-                } else {
-                    const uint32_t x = halves_from(w, t0, t1, 2 * B), y = halves_from(w, t0 + 2 * B, t1 + 2 * B, 2 * B);
-                    f[k][0] = field<B, 0>(x);
-                    f[k][1] = field<B, 1>(x);
-                    f[k][2] = field<B, 0>(y);
-                    f[k][3] = field<B, 1>(y);
-                }
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    f[k][i] = h2_bits(__hsub2(bits_h2(f[k][i]), bits_h2(Fld<B>::zero(i % Fld<B>::N))));
+        for (int k = 0; k < 2; ++k) {
+            const int t0 = (2 * k) * UT + unit, t1 = (2 * k + 1) * UT + unit;
+            if constexpr (B <= 4) {
+                const uint32_t x = halves_from(w, t0, t1, 4 * B);
+                f[k][0] = field<B, 0>(x);
+                f[k][1] = field<B, 1>(x);
+                f[k][2] = field<B, 2 % Fld<B>::N>(x);
+                f[k][3] = field<B, 3 % Fld<B>::N>(x);
+            } else {
+                const uint32_t x = halves_from(w, t0, t1, 2 * B), y = halves_from(w, t0 + 2 * B, t1 + 2 * B, 2 * B);
+                f[k][0] = field<B, 0>(x);
+                f[k][1] = field<B, 1>(x);
+                f[k][2] = field<B, 0>(y);
+                f[k][3] = field<B, 1>(y);
             }
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                mma_f16(acc[nt][2 * g], f[0][0], f[0][1], f[1][0], f[1][1], b0[gi][nt], b1[gi][nt]);
-                mma_f16(acc[nt][2 * g + 1], f[0][2], f[0][3], f[1][2], f[1][3], b0[gi][nt], b1[gi][nt]);
-            }
+            for (int i = 0; i < 4; ++i)
+                f[k][i] = h2_bits(__hsub2(bits_h2(f[k][i]), bits_h2(Fld<B>::zero(i % Fld<B>::N))));
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            mma_f16(acc[nt][2 * g], f[0][0], f[0][1], f[1][0], f[1][1], b0[nt], b1[nt]);
+            mma_f16(acc[nt][2 * g + 1], f[0][2], f[0][3], f[1][2], f[1][3], b0[nt], b1[nt]);
         }
     }
+}
+
+template <int D, int NT, int B, bool Masked>
+QG_DEV void output_tile(const uint8_t* part, int lane, const uint32_t (&p)[2][NT][2], float (&acc)[NT][D / 16][4]) {
+    output_half<D, NT, B, Masked>(part, 0, lane, p[0], acc);
+    output_half<D, NT, B, Masked>(part, 1, lane, p[1], acc);
 }
 
 // largest V scale among this lane's share of the tile's, up to token slot `last`
@@ -672,7 +673,7 @@ QG_DEV void att_next(const KvAttend& a, AttCursor& c, bool more) {
 }
 
 // rotate back, divide and store one row held by a warp (E consecutive dims a lane)
-template <int D, bool BF16>
+template <int D>
 QG_DEV void store_row(const KvAttend& a, float (&o)[D / 32], float m, float l, int row0, int r, int head, int lane) {
     constexpr int E = D / 32;
     fwht_warp<E>(o, lane);
@@ -680,7 +681,7 @@ QG_DEV void store_row(const KvAttend& a, float (&o)[D / 32], float m, float l, i
     const float inv = l == 0.f ? 0.f : 1.f / (l * (float)D);
     uint16_t v[E];
 #pragma unroll
-    for (int i = 0; i < E; ++i) v[i] = kv_from_float<BF16>(o[i] * inv);
+    for (int i = 0; i < E; ++i) v[i] = att_out(a, o[i] * inv);
     uint16_t* p = reinterpret_cast<uint16_t*>(a.out.p) + (row0 + tok) * a.out.row + hq * a.out.head + E * lane;
     if constexpr (E == 2) {
         *reinterpret_cast<uint32_t*>(p) = v[0] | (uint32_t)v[1] << 16;
@@ -693,8 +694,15 @@ QG_DEV void store_row(const KvAttend& a, float (&o)[D / 32], float m, float l, i
         a.lse[(int64_t)(row0 + tok) * a.q_heads + hq] = (m + log2f(l)) * 0.6931471805599453f;
 }
 
-template <int D, int NT, bool BF16>
+// KB, VB: the widths, or 0 where they are read from `a`.  Known widths make a tile's
+// work one run of instructions that hides the softmax's latency behind the codes' masks:
+// 131072 tokens at 4 bits 50 us against 56.5; they are built for 4/4 and 8/8.
+template <int D, int NT, int KB, int VB>
 __global__ void __launch_bounds__(AttCfg<D, NT>::T, 1) kv_attend_kernel(KvAttend a) {
+    if constexpr (KB > 0) {
+        a.pg.kb = KB;
+        a.pg.vb = VB;
+    }
     using C = AttCfg<D, NT>;
     constexpr int W = C::W, G = C::G, RB = C::RB, E = D / 32, T = C::T;
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -838,7 +846,7 @@ __global__ void __launch_bounds__(AttCfg<D, NT>::T, 1) kv_attend_kernel(KvAttend
     if (shared_q)
         for (int i = 0; i < items; ++i)
             for (int r = (warp + W - i * RB % W) % W; r < RB; r += W)
-                rotate_query<D, NT, BF16>(a, raw + (i * RB + r) * D, areas + i * C::QFloats, r >> 3, r & 7, lane);
+                rotate_query<D, NT>(a, raw + (i * RB + r) * D, areas + i * C::QFloats, r >> 3, r & 7, lane);
     __syncthreads();
 
     // ---- one warp's run, item by item
@@ -853,7 +861,7 @@ __global__ void __launch_bounds__(AttCfg<D, NT>::T, 1) kv_attend_kernel(KvAttend
         if (shared_q)
             load_queries<D, NT>(areas + my_item * C::QFloats, lane, q);
         else
-            rotate_queries<D, NT, BF16>(a, cs.row0, rows, r_base, cc.h, lane, q);
+            rotate_queries<D, NT>(a, cs.row0, rows, r_base, cc.h, lane, q);
         ++my_item;
         const int lo_pos = cs.pos0 + r_base / a.group;
         const int hi_pos = cs.pos0 + (min(r_base + RB, rows) - 1) / a.group;
@@ -885,7 +893,10 @@ __global__ void __launch_bounds__(AttCfg<D, NT>::T, 1) kv_attend_kernel(KvAttend
             const uint8_t* rec = ring + rec_at;
             const uint8_t* vpart = rec + k_bytes;
             {
-                switch (a.pg.kb) {
+                if constexpr (KB > 0) {
+                    scores_tile<D, NT, KB>(rec, lane, q, s);
+                } else {
+                    switch (a.pg.kb) {
 #define QG_SCORES(B)                            \
     case B:                                     \
         scores_tile<D, NT, B>(rec, lane, q, s); \
@@ -897,6 +908,7 @@ __global__ void __launch_bounds__(AttCfg<D, NT>::T, 1) kv_attend_kernel(KvAttend
                     QG_SCORES(6)
                     QG_SCORES(8)
 #undef QG_SCORES
+                    }
                 }
             }
             {
@@ -979,24 +991,28 @@ __global__ void __launch_bounds__(AttCfg<D, NT>::T, 1) kv_attend_kernel(KvAttend
                         p[h][nt][0] = movm_trans(h2_bits(__floats2half2_rn(w[h][nt][0], w[h][nt][1])));
                         p[h][nt][1] = movm_trans(h2_bits(__floats2half2_rn(w[h][nt][2], w[h][nt][3])));
                     }
-                switch (a.pg.vb) {
-#define QG_OUTPUT(B)                                                   \
-    case B:                                                            \
-        if (masked) {                                                  \
-            output_half<D, NT, B, true>(vpart, 0, lane, p[0], acc);  \
-            output_half<D, NT, B, true>(vpart, 1, lane, p[1], acc);  \
-        } else {                                                       \
-            output_half<D, NT, B, false>(vpart, 0, lane, p[0], acc); \
-            output_half<D, NT, B, false>(vpart, 1, lane, p[1], acc); \
-        }                                                              \
+                if constexpr (VB > 0) {
+                    if (masked)
+                        output_tile<D, NT, VB, true>(vpart, lane, p, acc);
+                    else
+                        output_tile<D, NT, VB, false>(vpart, lane, p, acc);
+                } else {
+                    switch (a.pg.vb) {
+#define QG_OUTPUT(B)                                               \
+    case B:                                                        \
+        if (masked)                                                \
+            output_tile<D, NT, B, true>(vpart, lane, p, acc);      \
+        else                                                       \
+            output_tile<D, NT, B, false>(vpart, lane, p, acc);     \
         break;
-                    QG_OUTPUT(2)
-                    QG_OUTPUT(3)
-                    QG_OUTPUT(4)
-                    QG_OUTPUT(5)
-                    QG_OUTPUT(6)
-                    QG_OUTPUT(8)
+                        QG_OUTPUT(2)
+                        QG_OUTPUT(3)
+                        QG_OUTPUT(4)
+                        QG_OUTPUT(5)
+                        QG_OUTPUT(6)
+                        QG_OUTPUT(8)
 #undef QG_OUTPUT
+                    }
                 }
             }
             __syncwarp();
@@ -1082,7 +1098,7 @@ __global__ void __launch_bounds__(AttCfg<D, NT>::T, 1) kv_attend_kernel(KvAttend
                         for (int g = 0; g < G; ++g) {
                             uint16_t v[4];
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) v[i] = kv_from_float<BF16>(x[g][i] * inv);
+                            for (int i = 0; i < 4; ++i) v[i] = att_out(a, x[g][i] * inv);
                             *reinterpret_cast<uint2*>(o + 32 * g) =
                                 make_uint2(v[0] | (uint32_t)v[1] << 16, v[2] | (uint32_t)v[3] << 16);
                         }
@@ -1219,7 +1235,7 @@ __global__ void __launch_bounds__(AttCfg<D, NT>::T, 1) kv_attend_kernel(KvAttend
         float o[E];
 #pragma unroll
         for (int k = 0; k < E; ++k) o[k] = slot_of(f)[r * C::OS + E * lane + k];
-        store_row<D, BF16>(a, o, stats[r * 2 * W + f], stats[(RB + r) * 2 * W + f], s.row0, g.rb * RB + r, g.head, lane);
+        store_row<D>(a, o, stats[r * 2 * W + f], stats[(RB + r) * 2 * W + f], s.row0, g.rb * RB + r, g.head, lane);
     }
     if (wholes == heads) return;
     __syncthreads();
@@ -1275,7 +1291,7 @@ __global__ void __launch_bounds__(AttCfg<D, NT>::T, 1) kv_attend_kernel(KvAttend
             float o[E];
 #pragma unroll
             for (int k = 0; k < E; ++k) o[k] = rowbuf[r * D + E * lane + k];
-            store_row<D, BF16>(a, o, stats[r * 2 * W], stats[(RB + r) * 2 * W], s.row0, g.rb * RB + r, g.head, lane);
+            store_row<D>(a, o, stats[r * 2 * W], stats[(RB + r) * 2 * W], s.row0, g.rb * RB + r, g.head, lane);
         }
     }
 }

@@ -32,7 +32,7 @@ struct DeviceInfo {
     bool int_attr[3] = {false, false, false};
     bool gemm_attr[2] = {false, false};
     bool quant_attr = false;
-    bool attend_attr[3][2][2] = {};  // [head size][row tiles][bf16]
+    bool attend_attr[3][2][3] = {};  // [head size][row tiles][widths]
 };
 
 DeviceInfo g_devs[64];
@@ -953,7 +953,7 @@ size_t attend_ws_bytes(int D, int sms) {
     return kAttendTicketBytes + (size_t)sms * 2 * rows * (D + 2) * 4;
 }
 
-template <int D, int NT, bool BF16>
+template <int D, int NT, int KB, int VB>
 int launch_attend(KvAttend a, DeviceInfo* dev, bool* attr, cudaStream_t s) {
     using C = AttCfg<D, NT>;
     constexpr size_t most = 226 * 1024;  // 227 KB a CTA, some of it static
@@ -963,7 +963,7 @@ int launch_attend(KvAttend a, DeviceInfo* dev, bool* attr, cudaStream_t s) {
     a.ring_bytes = (int)((std::max(a.stages * rec, (size_t)C::SlotBytes) + 127) / 128 * 128);
     if (a.stages < 1 || (size_t)a.ring_bytes > room) return QGEMM_ERR_UNSUPPORTED;
     if (!*attr) {  // a per-device setting
-        if (cudaFuncSetAttribute(kv_attend_kernel<D, NT, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        if (cudaFuncSetAttribute(kv_attend_kernel<D, NT, KB, VB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  (int)most) != cudaSuccess) {
             cudaGetLastError();
             return QGEMM_ERR_CUDA;
@@ -971,7 +971,7 @@ int launch_attend(KvAttend a, DeviceInfo* dev, bool* attr, cudaStream_t s) {
         *attr = true;
     }
     static_assert(C::MaxCtas * 4 <= kAttendTicketBytes, "a ticket for each CTA");
-    kv_attend_kernel<D, NT, BF16><<<std::min(dev->sms, C::MaxCtas), C::T, C::RingAt + C::W * a.ring_bytes, s>>>(a);
+    kv_attend_kernel<D, NT, KB, VB><<<std::min(dev->sms, C::MaxCtas), C::T, C::RingAt + C::W * a.ring_bytes, s>>>(a);
     return launch_status();
 }
 
@@ -1374,12 +1374,16 @@ int qgemm_kv_attend(const qgemm_kv_cache* cache, const qgemm_kv_batch* batch, in
     a.tickets = static_cast<unsigned int*>(d_ws);
     a.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(d_ws) + kAttendTicketBytes);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const bool bf = dtype == QGEMM_BF16;
+    a.bf16 = dtype == QGEMM_BF16;
     const int nt = attend_row_tiles(D, a.bt.rows, a.bt.num_seqs, a.group);
-#define QG_ATTEND(DD, NT, I)                                                                  \
-    if (D == DD && nt == NT)                                                                  \
-        return bf ? launch_attend<DD, NT, true>(a, dev, &dev->attend_attr[I][NT - 1][1], s)   \
-                  : launch_attend<DD, NT, false>(a, dev, &dev->attend_attr[I][NT - 1][0], s);
+    const int known = a.pg.kb != a.pg.vb ? 0 : a.pg.kb == 4 ? 1 : a.pg.kb == 8 ? 2 : 0;
+#define QG_ATTEND(DD, NT, I)                                                                 \
+    if (D == DD && nt == NT) {                                                               \
+        bool* attr = &dev->attend_attr[I][NT - 1][known];                                    \
+        return known == 1   ? launch_attend<DD, NT, 4, 4>(a, dev, attr, s)                   \
+               : known == 2 ? launch_attend<DD, NT, 8, 8>(a, dev, attr, s)                   \
+                            : launch_attend<DD, NT, 0, 0>(a, dev, attr, s);                  \
+    }
     QG_ATTEND(64, 1, 0)
     QG_ATTEND(64, 2, 0)
     QG_ATTEND(128, 1, 1)
