@@ -79,23 +79,6 @@ QG_DEV uint16_t kv_from_float(float v) {
     return __half_as_ushort(__float2half_rn(v));
 }
 
-// Sequence of row t (the last b with cu[b] <= t), found by the whole warp 32
-// entries at a time; -1 behind the last sequence's rows.
-QG_DEV int kv_find_seq(const int32_t* cu, int num_seqs, int t, int lane) {
-    int lo = 0, n = num_seqs + 1;  // the answer's entry is the last of cu[lo, lo + n) that is <= t
-    if (t < cu[0]) return -1;
-    while (n > 1) {
-        const int step = (n + 31) / 32;
-        const int i = lane * step;
-        const bool le = i < n && cu[lo + i] <= t;
-        const int k = 31 - __clz(__ballot_sync(0xffffffffu, le));
-        if (k < 0) return -1;
-        lo += k * step;
-        n = min(step, n - k * step);
-    }
-    return lo < num_seqs ? lo : -1;
-}
-
 // Record of (sequence b, position pos, head), or null (with the error word set)
 // when the table has no valid page for it.
 QG_DEV uint8_t* kv_record(const KvPages& pg, const KvBatch& bt, int b, int pos, int head, int rec_bytes) {
@@ -109,25 +92,6 @@ QG_DEV uint8_t* kv_record(const KvPages& pg, const KvBatch& bt, int b, int pos, 
     return pg.base + page * pg.page_bytes + (int64_t)(head * tiles + in / kTileTokens) * rec_bytes;
 }
 
-// Lane, unit and first dims of unit n (0 .. D/8 - 1) of a token in slot t of
-// its tile: K unit n = 4 g + j, V unit n = 8 h + r.
-template <int D, bool KEY>
-QG_DEV void kv_unit(int n, int t, int& lane, int& unit, int& d0, int& d1) {
-    if constexpr (KEY) {
-        const int g = n >> 2, j = n & 3;
-        lane = 4 * (t & 7) + j;
-        unit = (t >> 3) * (D / 32) + g;
-        d0 = 32 * g + 8 * j;
-        d1 = d0 + 4;
-    } else {
-        const int h = n >> 3, r = n & 7;
-        lane = 4 * r + ((t >> 1) & 3);
-        unit = ((t >> 3) * 2 + (t & 1)) * (D / 64) + h;
-        d0 = 64 * h + 4 * r;
-        d1 = d0 + 32;
-    }
-}
-
 // place of token slot t's scale of group g in the record's scale part (halves)
 template <int D, bool KEY>
 QG_DEV int kv_scale_at(int t, int g) {
@@ -137,132 +101,197 @@ QG_DEV int kv_scale_at(int t, int g) {
 }
 
 // slot i of a K unit of 5 bits and more holds dim kv_wide(i) of the eight (its own inverse)
-QG_DEV int kv_wide(int i) { return (i & 4) ? ((i & 2) ? i : i - 2) : ((i & 2) ? i + 2 : i); }
+QG_DEV constexpr int kv_wide(int i) { return (i & 4) ? ((i & 2) ? i : i - 2) : ((i & 2) ? i + 2 : i); }
+
+// ---------------------------------------------------- blocks of a batch's rows
+// The new tokens of a sequence are cut where their positions are multiples of N
+// (8 or 32).  Sequence b's blocks are numbered from cu[b] / N + 2 b on: with n
+// rows it has at most (n - 2) / N + 2 of them, so numbers never meet, no sum over
+// the sequences is needed, and rows / N + 2 num_seqs numbers are enough.
+struct KvBlock {
+    int b, row0, pos0, first, end;  // sequence; its first row and that row's position; positions [first, end) of the block
+};
+
+template <int N>
+QG_DEV bool kv_block(const KvBatch& bt, int number, int lane, KvBlock& k) {
+    int lo = 0, n = bt.num_seqs;
+    while (n > 1) {  // the last sequence whose first number is <= number, 32 at a time
+        const int step = (n + 31) / 32, i = lane * step;
+        const bool le = i < n && max(bt.cu[lo + i], 0) / N + 2 * (lo + i) <= number;
+        const int m = max(31 - __clz(__ballot_sync(0xffffffffu, le)), 0);
+        lo += m * step;
+        n = min(step, n - m * step);
+    }
+    const int c0 = bt.cu[lo], c1 = bt.cu[lo + 1], at = number - (max(c0, 0) / N + 2 * lo);
+    if (c0 < 0 || at < 0) return false;
+    k.b = lo;
+    k.row0 = c0;
+    k.pos0 = bt.lens[lo] - c1 + c0;
+    const int rows = min(c1, bt.rows) - c0;  // rows that the operands have
+    if (rows <= 0) return false;
+    const int64_t start = (int64_t)(max(k.pos0, 0) / N + at) * N, end = (int64_t)k.pos0 + rows;
+    if (start >= end || start > 0x7fffff00) return false;
+    k.first = max((int)start, k.pos0);
+    k.end = (int)(end < start + N ? end : start + N);
+    return true;
+}
 
 // ------------------------------------------------------------------- append
-// One warp per (row, head, K or V): rotate, quantise (the steps of
-// kv_quant_kernel, so the same codes bit for bit) and store the token's units.
+// One warp per (8 positions, head, K or V); four lanes a token, lane 4 t + j
+// with dims 32 g + 8 j + i: it is also the token's lane of the K stream, and
+// holds the V streams' rows 2 j and 2 j + 1.  Butterflies in the order strides
+// 1, 2, ..., D / 2 (8 and 16 between the four lanes), each rounded to nearest:
+// the codes of kv_quant_kernel, bit for bit.  Codes are packed in registers and
+// stored in the widest pieces that a token owns (16 bytes of K, 8 of V at 128
+// dims and 4 bits; eight neighbouring tokens fill whole sectors).
+// Bound by instructions (about 25 a value), not by HBM.
+
+// bits [at, at + b) of a bit string in 32-bit words
+template <int NW>
+QG_DEV void put_bits(uint32_t (&w)[NW], int at, int b, uint32_t v) {
+    w[at >> 5] |= v << (at & 31);
+    if ((at & 31) + b > 32) w[(at >> 5) + 1] |= v >> (32 - (at & 31));
+}
+
+// store a token's PB bytes (words w) at byte y0 of stream `lane`
+template <int PB, int C, int NW>
+QG_DEV void put_stream(uint8_t* part, int lane, int y0, const uint32_t (&w)[NW]) {
+    constexpr int V = (PB % 16 == 0 && C == 16) ? 16 : (PB % 8 == 0 && C >= 8) ? 8 : PB % 4 == 0 ? 4 : PB % 2 == 0 ? 2 : 1;
+    constexpr int clog = C == 16 ? 4 : C == 8 ? 3 : 2;
+#pragma unroll
+    for (int y = 0; y < PB; y += V) {
+        uint8_t* p = part + kv_stream_at(lane, y0 + y, clog);
+        if constexpr (V == 16) *reinterpret_cast<uint4*>(p) = make_uint4(w[y / 4], w[y / 4 + 1], w[y / 4 + 2], w[y / 4 + 3]);
+        if constexpr (V == 8) *reinterpret_cast<uint2*>(p) = make_uint2(w[y / 4], w[y / 4 + 1]);
+        if constexpr (V == 4) *reinterpret_cast<uint32_t*>(p) = w[y / 4];
+        if constexpr (V == 2) *reinterpret_cast<uint16_t*>(p) = (uint16_t)(w[y / 4] >> (8 * (y % 4)));
+        if constexpr (V == 1) *p = (uint8_t)(w[y / 4] >> (8 * (y % 4)));
+    }
+}
+
+template <int D, int B, bool KEY>
+QG_DEV void put_token(uint8_t* part, int t, int lane, bool mine, float (&x)[D / 32][8]) {
+    constexpr int G = D / 32, z = 1 << (B - 1);
+    constexpr int half = D * B / 16, C = half % 16 == 0 ? 16 : half % 8 == 0 ? 8 : 4;
+    const int j = lane & 3, tt = t >> 3;
+    __half sh[G];
+    uint32_t code[G][8];
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+        float amax = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(x[g][i]));
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+        sh[g] = __float2half_rn(__fdiv_rn(amax, (float)(z - 1)));
+        const float s = __half2float(sh[g]);
+        const float inv = s == 0.f ? 0.f : __frcp_rn(s);  // the zero point everywhere where s is 0
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            // clamped first (whole bounds: the same as after), then rounded to nearest even by the
+            // addition of 1.5 2^23, whose low bits are then the integer
+            const float q = fminf(fmaxf(__fmul_rn(x[g][i], inv), (float)(-z)), (float)(z - 1));
+            code[g][i] = __float_as_uint(__fadd_rn(q, 12582912.f + (float)z)) & 0xffffu;
+        }
+    }
+    if (!mine) return;
+    if constexpr (KEY) {
+        constexpr int PB = G * B;  // the lane's units of all groups
+        uint32_t w[(PB + 3) / 4 + 1] = {};
+#pragma unroll
+        for (int g = 0; g < G; ++g)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) put_bits(w, g * 8 * B + i * B, B, code[g][B >= 5 ? kv_wide(i) : i]);
+        put_stream<PB, C>(part, lane, tt * PB, w);
+    } else {
+        constexpr int PB = D / 64 * B;
+        const int u = t & 1, jt = (t >> 1) & 3;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            uint32_t w[(PB + 3) / 4 + 1] = {};
+#pragma unroll
+            for (int h = 0; h < D / 64; ++h)
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    put_bits(w, h * 8 * B + i * B, B, code[2 * h + (i >> 2)][4 * e + (i & 3)]);
+            put_stream<PB, C>(part, 4 * (2 * j + e) + jt, (2 * tt + u) * PB, w);
+        }
+    }
+    __half* sc = reinterpret_cast<__half*>(part + 4 * D * B);
+#pragma unroll
+    for (int g = 0; g < G; ++g)
+        if ((g & 3) == j) sc[kv_scale_at<D, KEY>(t, g)] = sh[g];
+}
+
 template <int D, bool BF16>
 __global__ void __launch_bounds__(32 * kKvWarps) kv_append_kernel(KvPages pg, KvBatch bt, KvRows k, KvRows v) {
-    constexpr int E = D / 32, G = 32 / E;
-    __shared__ uint8_t sh_codes[kKvWarps][D];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t item = (int64_t)blockIdx.x * kKvWarps + warp;
+    constexpr int G = D / 32;
+    const int lane = threadIdx.x & 31, j = lane & 3;
+    // K and V of one head are neighbours, heads of one block of rows too
+    const int64_t item = (int64_t)blockIdx.x * kKvWarps + (threadIdx.x >> 5);
     const bool key = (item & 1) == 0;
-    const int64_t th = item >> 1;
-    const int row = (int)(th / pg.heads), head = (int)(th - (int64_t)row * pg.heads);
-    if (row >= bt.rows) return;
-    const int b = kv_find_seq(bt.cu, bt.num_seqs, row, lane);
-    if (b < 0) return;
-    const int pos = bt.lens[b] - bt.cu[b + 1] + row;
-    if (pos < 0) return;
-    const int rb = kv_record_bytes<D>(pg.kb, pg.vb);
-    uint8_t* rec = kv_record(pg, bt, b, pos, head, rb);
+    const int64_t bh = item >> 1, number = bh / pg.heads;
+    const int head = (int)(bh - number * pg.heads);
+    KvBlock blk;
+    if (number >= (int64_t)bt.rows / 8 + 2ll * bt.num_seqs || !kv_block<8>(bt, (int)number, lane, blk)) return;
+    const int pos = (blk.first & ~7) + (lane >> 2);
+    const bool mine = pos >= blk.first && pos < blk.end;
+    uint8_t* rec = kv_record(pg, bt, blk.b, blk.first, head, kv_record_bytes<D>(pg.kb, pg.vb));
     if (!rec) return;
     const KvRows& src = key ? k : v;
-    const uint16_t* p = reinterpret_cast<const uint16_t*>(src.p) + row * src.row + head * src.head + E * lane;
-    float x[E];
+    const int64_t row = blk.row0 + (mine ? pos : blk.first) - blk.pos0;
+    const uint16_t* p = reinterpret_cast<const uint16_t*>(src.p) + row * src.row + head * src.head + 8 * j;
+    float x[G][8];
 #pragma unroll
-    for (int i = 0; i < E; ++i) x[i] = kv_to_float<BF16>(p[i]);
-    fwht_warp<E>(x, lane);
-    const int bits = key ? pg.kb : pg.vb, z = 1 << (bits - 1);
-    float amax = 0.f;
+    for (int g = 0; g < G; ++g) {
+        const uint4 u = __ldg(reinterpret_cast<const uint4*>(p + 32 * g));
+        const uint32_t q[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-    for (int i = 0; i < E; ++i) amax = fmaxf(amax, fabsf(x[i]));
-#pragma unroll
-    for (int o = 1; o < G; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    const __half sh = __float2half_rn(__fdiv_rn(amax, (float)(z - 1)));
-    const float s = __half2float(sh);
-    const float inv = (s == 0.f) ? 0.f : __frcp_rn(s);
-#pragma unroll
-    for (int i = 0; i < E; ++i) {
-        float tq = rintf(__fmul_rn(x[i], inv));
-        if (tq != tq) tq = 0.f;
-        tq = fminf(fmaxf(tq, (float)(-z)), (float)(z - 1));
-        sh_codes[warp][E * lane + i] = (uint8_t)((int)tq + z);
+        for (int i = 0; i < 8; ++i)
+            x[g][i] = kv_to_float<BF16>((uint16_t)((i & 1) ? q[i / 2] >> 16 : q[i / 2] & 0xffffu));
     }
-    __syncwarp();
+#pragma unroll
+    for (int st = 1; st < D; st <<= 1)
+#pragma unroll
+        for (int g = 0; g < G; ++g)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                if (st < 8) {
+                    if (i & st) continue;
+                    const float a = x[g][i], c = x[g][i | (st & 7)];
+                    x[g][i] = __fadd_rn(a, c);
+                    x[g][i | (st & 7)] = __fsub_rn(a, c);
+                } else if (st < 32) {
+                    const float o = __shfl_xor_sync(0xffffffffu, x[g][i], st / 8);
+                    x[g][i] = (lane & (st / 8)) ? __fsub_rn(o, x[g][i]) : __fadd_rn(x[g][i], o);
+                } else {
+                    if (g & (st / 32)) continue;
+                    const float a = x[g][i], c = x[(g | (st / 32)) % G][i];
+                    x[g][i] = __fadd_rn(a, c);
+                    x[(g | (st / 32)) % G][i] = __fsub_rn(a, c);
+                }
+            }
     const int t = pos & (kTileTokens - 1);
-    uint8_t* part = key ? rec : rec + 4 * D * pg.kb + 2 * D;
-    if (lane < D / 8) {
-        int l, unit, d0, d1;
-        if (key)
-            kv_unit<D, true>(lane, t, l, unit, d0, d1);
-        else
-            kv_unit<D, false>(lane, t, l, unit, d0, d1);
-        uint64_t w = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int m = (key && bits >= 5) ? kv_wide(i) : i;
-            const int d = (m < 4 ? d0 + m : d1 + m - 4);
-            w |= (uint64_t)sh_codes[warp][d] << (i * bits);
+    if (key) {
+        switch (pg.kb) {
+            case 2: put_token<D, 2, true>(rec, t, lane, mine, x); break;
+            case 3: put_token<D, 3, true>(rec, t, lane, mine, x); break;
+            case 4: put_token<D, 4, true>(rec, t, lane, mine, x); break;
+            case 5: put_token<D, 5, true>(rec, t, lane, mine, x); break;
+            case 6: put_token<D, 6, true>(rec, t, lane, mine, x); break;
+            default: put_token<D, 8, true>(rec, t, lane, mine, x); break;
         }
-        const int clog = kv_chunk_log2<D>(bits);
-        for (int i = 0; i < bits; ++i) part[kv_stream_at(l, unit * bits + i, clog)] = (uint8_t)(w >> (8 * i));
-    }
-    if (lane % G == 0) {
-        const int g = lane / G;
-        __half* sc = reinterpret_cast<__half*>(part + 4 * D * bits);
-        sc[key ? kv_scale_at<D, true>(t, g) : kv_scale_at<D, false>(t, g)] = sh;
-    }
-}
-
-// Rotated values of token slot t: this lane's E dims E lane .. E lane + E - 1.
-// sh: D bytes of the warp's own.
-template <int D, bool KEY>
-QG_DEV void kv_load_token(const uint8_t* rec, int t, int kb, int vb, uint8_t* sh, int lane, float (&x)[D / 32]) {
-    constexpr int E = D / 32;
-    const int bits = KEY ? kb : vb, z = 1 << (bits - 1);
-    const uint8_t* part = KEY ? rec : rec + 4 * D * kb + 2 * D;
-    __syncwarp();
-    if (lane < D / 8) {
-        int l, unit, d0, d1;
-        kv_unit<D, KEY>(lane, t, l, unit, d0, d1);
-        const int clog = kv_chunk_log2<D>(bits);
-        uint64_t w = 0;
-        for (int i = 0; i < bits; ++i) w |= (uint64_t)part[kv_stream_at(l, unit * bits + i, clog)] << (8 * i);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int m = (KEY && bits >= 5) ? kv_wide(i) : i;
-            sh[m < 4 ? d0 + m : d1 + m - 4] = (uint8_t)((w >> (i * bits)) & ((1u << bits) - 1u));
+    } else {
+        uint8_t* part = rec + 4 * D * pg.kb + 2 * D;
+        switch (pg.vb) {
+            case 2: put_token<D, 2, false>(part, t, lane, mine, x); break;
+            case 3: put_token<D, 3, false>(part, t, lane, mine, x); break;
+            case 4: put_token<D, 4, false>(part, t, lane, mine, x); break;
+            case 5: put_token<D, 5, false>(part, t, lane, mine, x); break;
+            case 6: put_token<D, 6, false>(part, t, lane, mine, x); break;
+            default: put_token<D, 8, false>(part, t, lane, mine, x); break;
         }
     }
-    __syncwarp();
-    const __half* sc = reinterpret_cast<const __half*>(part + 4 * D * bits);
-    const float s = __half2float(sc[kv_scale_at<D, KEY>(t, E * lane / 32)]);
-#pragma unroll
-    for (int i = 0; i < E; ++i) x[i] = __fmul_rn((float)((int)sh[E * lane + i] - z), s);  // exact
-}
-
-// ------------------------------------------------------------------- gather
-// One warp per (row, head, K or V): v' = H_D u' / D.
-template <int D, bool BF16>
-__global__ void __launch_bounds__(32 * kKvWarps) kv_gather_kernel(KvPages pg, KvBatch bt, KvRows k, KvRows v) {
-    constexpr int E = D / 32;
-    __shared__ uint8_t sh_codes[kKvWarps][D];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t item = (int64_t)blockIdx.x * kKvWarps + warp;
-    const bool key = (item & 1) == 0;
-    const int64_t th = item >> 1;
-    const int row = (int)(th / pg.heads), head = (int)(th - (int64_t)row * pg.heads);
-    if (row >= bt.rows) return;
-    const int b = kv_find_seq(bt.cu, bt.num_seqs, row, lane);
-    if (b < 0) return;
-    const int pos = bt.lens[b] - bt.cu[b + 1] + row;
-    if (pos < 0) return;
-    const uint8_t* rec = kv_record(pg, bt, b, pos, head, kv_record_bytes<D>(pg.kb, pg.vb));
-    if (!rec) return;
-    float x[E];
-    const int t = pos & (kTileTokens - 1);
-    if (key)
-        kv_load_token<D, true>(rec, t, pg.kb, pg.vb, sh_codes[warp], lane, x);
-    else
-        kv_load_token<D, false>(rec, t, pg.kb, pg.vb, sh_codes[warp], lane, x);
-    fwht_warp<E>(x, lane);
-    const KvRows& dst = key ? k : v;
-    uint16_t* p = reinterpret_cast<uint16_t*>(dst.p) + row * dst.row + head * dst.head + E * lane;
-#pragma unroll
-    for (int i = 0; i < E; ++i) p[i] = kv_from_float<BF16>(__fmul_rn(x[i], 1.f / (float)D));
 }
 
 }  // namespace qg

@@ -19,6 +19,7 @@
 #include "kv_cache.cuh"
 #include "kv_paged.cuh"
 #include "kv_attend.cuh"
+#include "kv_gather.cuh"
 
 namespace {
 
@@ -921,15 +922,20 @@ int kv_move(bool append, const qgemm_kv_cache* cache, const qgemm_kv_batch* batc
     const int D = cache->head_dim;
     if ((st = kv_rows(d_k, krs, khs, bt.rows, pg.heads, D, !append, &k)) != QGEMM_OK) return st;
     if ((st = kv_rows(d_v, vrs, vhs, bt.rows, pg.heads, D, !append, &v)) != QGEMM_OK) return st;
-    const int64_t items = 2 * (int64_t)bt.rows * pg.heads, ctas = (items + kKvWarps - 1) / kKvWarps;
+    // blocks of 8 positions (append) or 32 (gather), see kv_block
+    const int64_t numbers = bt.rows / (append ? 8 : kTileTokens) + 2ll * bt.num_seqs;
+    const int64_t ctas = (2 * numbers * pg.heads + kKvWarps - 1) / kKvWarps;
     if (ctas > 0x7fffffff) return QGEMM_ERR_SHAPE;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool bf = dtype == QGEMM_BF16;
-#define QG_KV_MOVE(DD)                                                                         \
-    if (D == DD) {                                                                             \
-        auto f = append ? (bf ? kv_append_kernel<DD, true> : kv_append_kernel<DD, false>)      \
-                        : (bf ? kv_gather_kernel<DD, true> : kv_gather_kernel<DD, false>);     \
-        f<<<(unsigned)ctas, 32 * kKvWarps, 0, s>>>(pg, bt, k, v);                              \
+#define QG_KV_MOVE(DD)                                                                             \
+    if (D == DD) {                                                                                 \
+        if (append) {                                                                              \
+            auto f = bf ? kv_append_kernel<DD, true> : kv_append_kernel<DD, false>;                \
+            f<<<(unsigned)ctas, 32 * kKvWarps, 0, s>>>(pg, bt, k, v);                              \
+        } else {                                                                                   \
+            kv_gather_kernel<DD><<<(unsigned)ctas, 32 * kKvWarps, 0, s>>>(pg, bt, k, v, bf);       \
+        }                                                                                          \
     }
     QG_KV_MOVE(64)
     QG_KV_MOVE(128)
