@@ -377,7 +377,7 @@ class KVCache:
         if pages.dim() < 1 or pages.shape[0] < 1 or pages.numel() != pages.shape[0] * words:
             _shape_error(f"pages must be [num_pages >= 1, ...] with {words} words a page, got {tuple(pages.shape)}")
         ptr = _dev(pages, (torch.int32, torch.uint32), "pages")
-        self.pages, self.device = pages, pages.device
+        self.pages, self.device_index = pages, pages.get_device()
         self.page_size, self.kv_heads, self.head_dim = int(page_size), int(kv_heads), int(head_dim)
         self.k_bits, self.v_bits = int(k_bits), int(v_bits)
         self._c = _CacheStruct(ptr, pages.shape[0], self.page_size, self.kv_heads, self.head_dim, self.k_bits,
@@ -402,33 +402,44 @@ class KVBatch:
     def __init__(self, block_table, seq_lens, cu_new):
         import torch
         i32 = torch.int32
-        if block_table.dim() != 2 or seq_lens.dim() != 1 or cu_new.dim() != 1:
+        shape = block_table.shape
+        if len(shape) != 2 or seq_lens.dim() != 1 or cu_new.dim() != 1:
             _shape_error("block_table must be [B, max_pages], seq_lens [B], cu_new [B + 1]")
-        B, P = block_table.shape
+        B, P = shape
         if seq_lens.shape[0] != B or cu_new.shape[0] != B + 1:
             _shape_error(f"block_table has {B} rows, seq_lens {seq_lens.shape[0]} entries, "
                          f"cu_new {cu_new.shape[0]} (B + 1 expected)")
-        if block_table.is_cuda and (block_table.dtype is i32) and (P <= 1 or block_table.stride(1) == 1):
-            stride = block_table.stride(0) if B > 1 else P
-            if stride < P:
-                _shape_error("block_table's rows overlap")
-            table = block_table.data_ptr()
-        else:
-            table, stride = _dev(block_table, i32, "block_table"), P  # names what is wrong
-        self.device = block_table.device
-        if seq_lens.device != self.device or cu_new.device != self.device:
+        if not block_table.is_cuda:
+            raise TypeError("block_table must be a CUDA tensor")
+        for t, name in ((block_table, "block_table"), (seq_lens, "seq_lens"), (cu_new, "cu_new")):
+            if t.dtype is not i32:
+                raise TypeError(f"{name} must have dtype {i32}, got {t.dtype}")
+        dev = block_table.get_device()
+        if seq_lens.get_device() != dev or cu_new.get_device() != dev:
             raise ValueError("block_table, seq_lens and cu_new must be on one device")
+        if not seq_lens.is_contiguous() or not cu_new.is_contiguous():
+            raise ValueError("seq_lens and cu_new must be contiguous")
+        stride = P
+        if not block_table.is_contiguous():
+            stride, es = block_table.stride()
+            if (es != 1 and P > 1) or (stride < P and B > 1):
+                raise ValueError("block_table's rows must be contiguous and apart")
+            stride = max(stride, P)
+        self.device_index = dev
         self._keep = (block_table, seq_lens, cu_new)
-        self._c = _BatchStruct(table, stride, _dev(seq_lens, i32, "seq_lens"), _dev(cu_new, i32, "cu_new"), B, P)
+        self._c = _BatchStruct(block_table.data_ptr(), stride, seq_lens.data_ptr(), cu_new.data_ptr(), B, P)
         self._ref = ctypes.byref(self._c)
 
 
-def _kv_rows(t, name, heads, D, dtype):
+def _kv_rows(t, name, heads, D, dtype, dev):
     """Address and strides of a [rows, heads, D] operand."""
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != D:
-        _shape_error(f"{name} must be [rows, {heads}, {D}], got {tuple(t.shape)}")
-    if not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
+    shape = t.shape
+    if len(shape) != 3 or shape[1] != heads or shape[2] != D:
+        _shape_error(f"{name} must be [rows, {heads}, {D}], got {tuple(shape)}")
+    if t.get_device() != dev:
+        if not t.is_cuda:
+            raise TypeError(f"{name} must be a CUDA tensor")
+        raise ValueError(f"{name} on {t.device}, the cache on cuda:{dev}")
     if t.dtype is not dtype:
         raise TypeError(f"{name} must have dtype {dtype}, got {t.dtype}")
     rs, hs, es = t.stride()
@@ -437,35 +448,32 @@ def _kv_rows(t, name, heads, D, dtype):
     return t.data_ptr(), rs, hs
 
 
-def _kv_dtype(t, name):
+def _kv_call(cache, batch, t, name, stream):
+    """What every call checks first: the operands' type, one device, the stream (its address)."""
     import torch
     if t.dtype is torch.float16:
-        return QGEMM_F16
-    if t.dtype is torch.bfloat16:
-        return QGEMM_BF16
-    raise TypeError(f"{name} must be float16 or bfloat16, got {t.dtype}")
+        dt = QGEMM_F16
+    elif t.dtype is torch.bfloat16:
+        dt = QGEMM_BF16
+    else:
+        raise TypeError(f"{name} must be float16 or bfloat16, got {t.dtype}")
+    dev = cache.device_index
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"cache on cuda:{dev}, but the current device is cuda:{torch.cuda.current_device()}")
+    if batch.device_index != dev:
+        raise ValueError(f"cache on cuda:{dev}, batch on cuda:{batch.device_index}")
+    return dt, dev, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
-def _kv_devices(cache, batch, *tensors):
-    import torch
-    dev = cache.device
-    if dev.index != torch.cuda.current_device():
-        raise ValueError(f"cache on {dev}, but the current device is cuda:{torch.cuda.current_device()}")
-    if batch.device != dev:
-        raise ValueError(f"cache on {dev}, batch on {batch.device}")
-    for t in tensors:
-        if t.device != dev:
-            raise ValueError(f"tensor on {t.device}, cache on {dev}")
-
-
-def _kv_move(fn, name, cache, batch, k, v, stream):
-    dt = _kv_dtype(k, "k")
-    kp, krs, khs = _kv_rows(k, "k", cache.kv_heads, cache.head_dim, k.dtype)
-    vp, vrs, vhs = _kv_rows(v, "v", cache.kv_heads, cache.head_dim, k.dtype)
-    if v.shape[0] != k.shape[0]:
-        _shape_error(f"k has {k.shape[0]} rows, v has {v.shape[0]}")
-    _kv_devices(cache, batch, k, v)
-    _ok(fn(cache._ref, batch._ref, k.shape[0], kp, krs, khs, vp, vrs, vhs, dt, _stream(stream)), name)
+def _kv_move(fn, where, cache, batch, k, v, stream):
+    dt, dev, st = _kv_call(cache, batch, k, "k", stream)
+    H, D = cache.kv_heads, cache.head_dim
+    kp, krs, khs = _kv_rows(k, "k", H, D, k.dtype, dev)
+    vp, vrs, vhs = _kv_rows(v, "v", H, D, k.dtype, dev)
+    T = k.shape[0]
+    if v.shape[0] != T:
+        _shape_error(f"k has {T} rows, v has {v.shape[0]}")
+    _ok(fn(cache._ref, batch._ref, T, kp, krs, khs, vp, vrs, vhs, dt, st), where)
 
 
 def qgemm_kv_append(k, v, cache, batch, stream=None):
@@ -487,27 +495,27 @@ def qgemm_kv_attend(q, cache, batch, out, ws, scale=None, window=0, lse=None, st
     [rows, q_heads].  scale defaults to D ** -0.5; window > 0 keeps the last
     `window` positions of each row.  ws: kv_workspace(cache, q_heads)."""
     import torch
-    dt = _kv_dtype(q, "q")
+    dt, dev, st = _kv_call(cache, batch, q, "q", stream)
     if q.dim() != 3:
         _shape_error("q must be [rows, q_heads, D]")
     T, Hq, D = q.shape
-    qp, qrs, qhs = _kv_rows(q, "q", Hq, cache.head_dim, q.dtype)
-    op, ors, ohs = _kv_rows(out, "out", Hq, cache.head_dim, q.dtype)
     if Hq == 0 or Hq % cache.kv_heads:
         _shape_error(f"q_heads = {Hq} is not a multiple of kv_heads = {cache.kv_heads}")
+    qp, qrs, qhs = _kv_rows(q, "q", Hq, cache.head_dim, q.dtype, dev)
+    op, ors, ohs = _kv_rows(out, "out", Hq, cache.head_dim, q.dtype, dev)
     if out.shape[0] != T:
         _shape_error(f"q has {T} rows, out has {out.shape[0]}")
-    if lse is None:
-        _kv_devices(cache, batch, q, out, ws)
-        lp = None
-    else:
+    lp = None
+    if lse is not None:
         if lse.dim() != 2 or lse.shape[0] != T or lse.shape[1] != Hq:
             _shape_error(f"lse must be [{T}, {Hq}], got {tuple(lse.shape)}")
-        _kv_devices(cache, batch, q, out, ws, lse)
-        lp = _dev(lse, torch.float32, "lse")
+        if lse.dtype is not torch.float32 or lse.get_device() != dev or not lse.is_contiguous():
+            raise TypeError(f"lse must be a contiguous float32 tensor on cuda:{dev}")
+        lp = lse.data_ptr()
+    if ws.dtype is not torch.uint8 or ws.get_device() != dev or not ws.is_contiguous():
+        raise TypeError(f"ws must be a contiguous uint8 tensor on cuda:{dev}")
     _ok(_lib.qgemm_kv_attend(cache._ref, batch._ref, T, qp, qrs, qhs, dt, Hq, D ** -0.5 if scale is None else scale,
-                             window, op, ors, ohs, lp, _dev(ws, torch.uint8, "ws"), ws.numel(), _stream(stream)),
-        "qgemm_kv_attend")
+                             window, op, ors, ohs, lp, ws.data_ptr(), ws.numel(), st), "qgemm_kv_attend")
     return out
 
 
@@ -517,7 +525,7 @@ def kv_workspace(cache, q_heads: int):
     n = int(_lib.qgemm_kv_attend_workspace_bytes(cache._ref, int(q_heads)))
     if n == 0:
         _shape_error(f"q_heads = {q_heads} is not a multiple of kv_heads = {cache.kv_heads}")
-    return torch.zeros(n, dtype=torch.uint8, device=cache.device)
+    return torch.zeros(n, dtype=torch.uint8, device=f"cuda:{cache.device_index}")
 
 
 def qgemm(x, perm, qw, scales, bits, offs, y, ws=None, stream=None):
