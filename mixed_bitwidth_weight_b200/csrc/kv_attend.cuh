@@ -85,7 +85,7 @@ struct AttCfg {
 // a slot's fragment: tiles [a, b) of the item whose first tile is number `item`
 struct AttFrag {
     long long item;
-    int seq, head, rb, tiles;  // the item; tiles = all its tiles, 0 = no fragment
+    int row0, rows, head, tiles;  // the item's rows: `rows` from row0 x group on, of KV head `head`; tiles 0: no fragment
 };
 static_assert(sizeof(AttFrag) == 24 && kAttMaxStages == 8, "the shared-memory layout");
 
@@ -672,17 +672,18 @@ QG_DEV void att_next(const KvAttend& a, AttCursor& c, bool more) {
     } while (c.s.nrb == 0 && c.b + 1 < a.bt.num_seqs);
 }
 
-// rotate back, divide and store one row held by a warp (E consecutive dims a lane)
+// rotate back, divide and store one row held by a warp (E consecutive dims a lane);
+// at: the row's number, (query row) x group + (head of the group)
 template <int D>
-QG_DEV void store_row(const KvAttend& a, float (&o)[D / 32], float m, float l, int row0, int r, int head, int lane) {
+QG_DEV void store_row(const KvAttend& a, float (&o)[D / 32], float m, float l, int at, int head, int lane) {
     constexpr int E = D / 32;
     fwht_warp<E>(o, lane);
-    const int tok = r / a.group, hq = head * a.group + (r - tok * a.group);
+    const int row = at / a.group, hq = head * a.group + (at - row * a.group);
     const float inv = l == 0.f ? 0.f : 1.f / (l * (float)D);
     uint16_t v[E];
 #pragma unroll
     for (int i = 0; i < E; ++i) v[i] = att_out(a, o[i] * inv);
-    uint16_t* p = reinterpret_cast<uint16_t*>(a.out.p) + (row0 + tok) * a.out.row + hq * a.out.head + E * lane;
+    uint16_t* p = reinterpret_cast<uint16_t*>(a.out.p) + (int64_t)row * a.out.row + hq * a.out.head + E * lane;
     if constexpr (E == 2) {
         *reinterpret_cast<uint32_t*>(p) = v[0] | (uint32_t)v[1] << 16;
     } else {
@@ -690,8 +691,7 @@ QG_DEV void store_row(const KvAttend& a, float (&o)[D / 32], float m, float l, i
         for (int i = 0; i < E; i += 4)
             *reinterpret_cast<uint2*>(p + i) = make_uint2(v[i] | (uint32_t)v[i + 1] << 16, v[i + 2] | (uint32_t)v[i + 3] << 16);
     }
-    if (a.lse && lane == 0)
-        a.lse[(int64_t)(row0 + tok) * a.q_heads + hq] = (m + log2f(l)) * 0.6931471805599453f;
+    if (a.lse && lane == 0) a.lse[(int64_t)row * a.q_heads + hq] = (m + log2f(l)) * 0.6931471805599453f;
 }
 
 // KB, VB: the widths, or 0 where they are read from `a`.  Known widths make a tile's
@@ -745,7 +745,7 @@ __global__ void __launch_bounds__(AttCfg<D, NT>::T, 1) kv_attend_kernel(KvAttend
     prefix[threadIdx.x] = before + inc - mine;
     __syncthreads();
     // two tiles a warp at least: a join across CTAs costs more than a second tile
-    const long long share = max((total + gridDim.x - 1) / gridDim.x, 2ll * W);
+    const long long share = max(div_ll(total + gridDim.x - 1, gridDim.x), 2ll * W);
     const long long cta0 = min(share * blockIdx.x, total), cta1 = min(cta0 + share, total);
     if (cta0 >= cta1) return;
     // warp w's first tile: shares differ by one at most
@@ -761,7 +761,7 @@ __global__ void __launch_bounds__(AttCfg<D, NT>::T, 1) kv_attend_kernel(KvAttend
         r += rb * RB;
         const uint16_t* p = nullptr;
         if (r < s.n * a.group) {
-            const int tok = r / a.group, hq = head * a.group + (r - tok * a.group);
+            const int tok = s.n == 1 ? 0 : r / a.group, hq = head * a.group + (r - tok * a.group);
             p = reinterpret_cast<const uint16_t*>(a.q.p) + (s.row0 + tok) * a.q.row + hq * a.q.head;
         }
         for (int i = lane * 8; i < D; i += 256) {  // 16 bytes a lane
@@ -771,9 +771,24 @@ __global__ void __launch_bounds__(AttCfg<D, NT>::T, 1) kv_attend_kernel(KvAttend
                 *reinterpret_cast<uint4*>(dst + i) = make_uint4(0, 0, 0, 0);
         }
     };
-    AttCursor pc, cc;  // the place of the copies, the place of the sums
+    // The warp's own place first: the first entries of its block table are on their way meanwhile.
+    const int lps = 31 - __clz(a.pg.page_size / kTileTokens);  // log2 tiles per page
+    AttCursor pc{}, cc;                                        // the place of the copies, the place of the sums
+    int page_base = 0, page_b = -1, page_id = 0;               // lane i: page page_base + i of sequence page_b
+    auto load_pages = [&](int pi) {
+        page_b = pc.b;
+        page_base = pi;
+        const int i = pi + lane;
+        page_id = i < a.bt.max_pages && ((int64_t)i << lps) * kTileTokens < pc.s.len
+                      ? a.bt.table[pc.b * a.bt.table_stride + i]
+                      : -1;
+    };
+    if (count > 0) {
+        att_seek<RB>(a, prefix, T, chunk, w0, pc);
+        load_pages((pc.s.t0 + pc.tile) >> lps);
+    }
+    cc = pc;
     int my_item = 0, items = 0;
-    bool found = count == 0;
     {
         AttCursor c;
         att_seek<RB>(a, prefix, T, chunk, cta0, c);
@@ -782,24 +797,15 @@ __global__ void __launch_bounds__(AttCfg<D, NT>::T, 1) kv_attend_kernel(KvAttend
             if (items < C::QN)
                 for (int r = (warp + W - items * RB % W) % W; r < RB; r += W)
                     fetch_row(c.s, c.h, c.rb, r, raw + (items * RB + r) * D);
-            if (!found && w0 < at + c.s.tiles) {
-                found = true;
-                my_item = items;
-                pc = c;
-                pc.tile = (int)(w0 - at);
-            }
+            if (w0 >= at) my_item = items;
             at += c.s.tiles;
             c.tile = c.s.tiles - 1;
             att_next<RB>(a, c, at < cta1);
         }
     }
     const bool shared_q = items <= C::QN;
-    if (!found) att_seek<RB>(a, prefix, T, chunk, w0, pc);
-    cc = pc;
 
     // ---- The ring: whole records, each warp its own.
-    const int lps = 31 - __clz(a.pg.page_size / kTileTokens);  // log2 tiles per page
-    int page_base = 0, page_b = -1, page_id = 0;               // lane i: page page_base + i of sequence page_b
     int left = count, page_left = 0;                           // tiles of the run, of the page, still to copy
     uint32_t bad = 0;                                          // stages whose tile has no page
     bool dead = false, has = false;
@@ -807,14 +813,7 @@ __global__ void __launch_bounds__(AttCfg<D, NT>::T, 1) kv_attend_kernel(KvAttend
     auto issue = [&](int s) {
         if (page_left == 0) {
             const int t = pc.s.t0 + pc.tile, pi = t >> lps, in = t & ((1 << lps) - 1);
-            if (page_b != pc.b || (uint32_t)(pi - page_base) >= 32u) {
-                page_b = pc.b;
-                page_base = pi;
-                const int i = pi + lane;
-                page_id = i < a.bt.max_pages && ((int64_t)i << lps) * kTileTokens < pc.s.len
-                              ? a.bt.table[pc.b * a.bt.table_stride + i]
-                              : -1;
-            }
+            if (page_b != pc.b || (uint32_t)(pi - page_base) >= 32u) load_pages(pi);
             const int page = __shfl_sync(0xffffffffu, page_id, pi - page_base);
             has = (uint32_t)page < (uint32_t)a.pg.num_pages && pc.s.len > 0;
             if (!has && pc.s.len > 0 && lane == 0) set_dev_error(QGEMM_DEV_BAD_PAGE);
@@ -1127,9 +1126,9 @@ __global__ void __launch_bounds__(AttCfg<D, NT>::T, 1) kv_attend_kernel(KvAttend
             if (lane == 0) {
                 // the item's first tile as a number of the call
                 fr.item = at - cc.tile;
-                fr.seq = cc.b;
+                fr.row0 = cs.row0 * a.group + r_base;
+                fr.rows = min(RB, rows - r_base);
                 fr.head = cc.h;
-                fr.rb = cc.rb;
                 fr.tiles = cs.tiles;
             }
         }
@@ -1230,12 +1229,11 @@ __global__ void __launch_bounds__(AttCfg<D, NT>::T, 1) kv_attend_kernel(KvAttend
     for (int i = warp; i < __popc(wholes) * RB; i += W) {
         const int f = __fns(wholes, 0, i / RB + 1), r = i % RB;
         const AttFrag& g = frags[f];
-        const AttSeq s = att_seq<RB>(a, g.seq);
-        if (g.rb * RB + r >= s.n * a.group) continue;
+        if (r >= g.rows) continue;
         float o[E];
 #pragma unroll
         for (int k = 0; k < E; ++k) o[k] = slot_of(f)[r * C::OS + E * lane + k];
-        store_row<D>(a, o, stats[r * 2 * W + f], stats[(RB + r) * 2 * W + f], s.row0, g.rb * RB + r, g.head, lane);
+        store_row<D>(a, o, stats[r * 2 * W + f], stats[(RB + r) * 2 * W + f], g.row0 + r, g.head, lane);
     }
     if (wholes == heads) return;
     __syncthreads();
@@ -1243,15 +1241,15 @@ __global__ void __launch_bounds__(AttCfg<D, NT>::T, 1) kv_attend_kernel(KvAttend
         const AttFrag g = frags[__ffs(hs) - 1];
         if (!sh_last[g.item < cta0 ? 0 : 1]) continue;
         const int c0 = (int)(g.item / share), c1 = (int)((g.item + g.tiles - 1) / share);
-        const AttSeq s = att_seq<RB>(a, g.seq);
         auto part_of = [&](int k) { return a.partial + ((size_t)k * 2 + (k == c0 ? 1 : 0)) * C::GSlot; };
         __syncthreads();
         for (int r = warp; r < RB; r += W) {
-            float ms[C::MaxCtas / 32], mx = -INFINITY, lt = 0.f;
+            float ms[C::MaxCtas / 32], ls[C::MaxCtas / 32], mx = -INFINITY, lt = 0.f;
 #pragma unroll
             for (int i = 0; i < C::MaxCtas / 32; ++i) {
                 const int k = c0 + lane + 32 * i;
                 ms[i] = k <= c1 ? __ldcg(part_of(k) + RB * D + r) : -INFINITY;
+                ls[i] = k <= c1 ? __ldcg(part_of(k) + RB * D + RB + r) : 0.f;
                 mx = fmaxf(mx, ms[i]);
             }
 #pragma unroll
@@ -1261,7 +1259,7 @@ __global__ void __launch_bounds__(AttCfg<D, NT>::T, 1) kv_attend_kernel(KvAttend
                 const int k = c0 + lane + 32 * i;
                 if (k > c1) continue;
                 const float w = ms[i] == mx ? 1.f : ex2(ms[i] - mx);
-                lt = fmaf(w, __ldcg(part_of(k) + RB * D + RB + r), lt);
+                lt = fmaf(w, ls[i], lt);
                 weights[r * C::MaxCtas + k - c0] = w;
             }
 #pragma unroll
@@ -1287,11 +1285,11 @@ __global__ void __launch_bounds__(AttCfg<D, NT>::T, 1) kv_attend_kernel(KvAttend
             *reinterpret_cast<float4*>(rowbuf + 4 * i) = o;
         }
         __syncthreads();
-        for (int r = warp; r < min(RB, s.n * a.group - g.rb * RB); r += W) {
+        for (int r = warp; r < g.rows; r += W) {
             float o[E];
 #pragma unroll
             for (int k = 0; k < E; ++k) o[k] = rowbuf[r * D + E * lane + k];
-            store_row<D>(a, o, stats[r * 2 * W], stats[(RB + r) * 2 * W], s.row0, g.rb * RB + r, g.head, lane);
+            store_row<D>(a, o, stats[r * 2 * W], stats[(RB + r) * 2 * W], g.row0 + r, g.head, lane);
         }
     }
 }
