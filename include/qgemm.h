@@ -268,7 +268,7 @@ typedef struct {
 typedef struct {
     const int32_t* d_block_table;
     int64_t table_stride;       /* elements between rows, >= max_pages             */
-    const int32_t* d_seq_lens;  /* [num_seqs]                                      */
+    const int32_t* d_seq_lens;  /* [num_seqs], each at most 2^30                   */
     const int32_t* d_cu_new;    /* [num_seqs + 1]                                  */
     int32_t num_seqs;           /* 0 .. 65535                                      */
     int32_t max_pages;          /* entries in a row of the table                   */

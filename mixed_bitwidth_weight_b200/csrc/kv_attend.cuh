@@ -57,7 +57,7 @@ constexpr float kAttNone = -3.4e38f;  // the weights' offset before any token: b
 
 template <int D, int NT>
 struct AttCfg {
-    static constexpr int W = D * NT <= 128 ? 8 : 7;  // warps: 255 registers a thread
+    static constexpr int W = D * NT <= 64 ? 12 : 8;   // warps: 168 registers a thread with 12, 255 with 8
     static constexpr int T = 32 * W;
     static constexpr int G = D / 32;
     static constexpr int RB = 8 * NT;                 // query rows of an item
@@ -518,62 +518,71 @@ QG_DEV void load_queries(const float* area, int lane, AttQ<D, NT>& q) {
 }
 
 // ------------------------------------------------------------------- output
-// acc += (codes of V) x (weights): half a tile.  p[nt][k]: weights of tokens
-// 16 half + 8 k + 2 j + {0, 1} for row n = lane / 4.
-template <int D, int NT, int B, bool Masked>
-QG_DEV void output_half(const uint8_t* part, int half, int lane, const uint32_t (&p)[NT][2],
-                        float (&acc)[NT][D / 16][4]) {
-    constexpr int G = D / 32, NW = D * B / 64, UT = D / 64 * 8 * B;  // bits of a token's units
+// A registers of half a tile's V codes, c - z, in units of their fields: f[g][k][i]
+// holds field i of group g's dims for tokens 16 half + 8 k + 2 j + {0, 1}.
+template <int D, int B>
+QG_DEV void v_fields(const uint8_t* part, int half, int lane, uint32_t (&f)[D / 32][2][4]) {
+    constexpr int G = D / 32, NW = D * B / 64, UT = D / 64 * 8 * B;  // UT: bits of a token's units
     uint32_t w[NW];
     load_words<D, B>(part, half, lane, w);
-    const uint8_t* scales = part + 4 * D * B + ((lane & 3) * G * 8 + 4 * half) * 2;
 #pragma unroll
     for (int g = 0; g < G; ++g) {
-        const uint2 su = *reinterpret_cast<const uint2*>(scales + g * 16);
-        uint32_t b0[NT], b1[NT];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            b0[nt] = h2_bits(__hmul2(bits_h2(p[nt][0]), bits_h2(su.x)));
-            b1[nt] = h2_bits(__hmul2(bits_h2(p[nt][1]), bits_h2(su.y)));
-            if constexpr (Masked) {  // a weight of 0 is 0 whatever the scale it meets
-                b0[nt] &= __hneu2_mask(bits_h2(p[nt][0]), bits_h2(0));
-                b1[nt] &= __hneu2_mask(bits_h2(p[nt][1]), bits_h2(0));
-            }
-        }
         const int unit = (g >> 1) * 8 * B + (g & 1) * 4 * B;  // this group's four codes in a token's units
-        uint32_t f[2][4];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
             const int t0 = (2 * k) * UT + unit, t1 = (2 * k + 1) * UT + unit;
             if constexpr (B <= 4) {
                 const uint32_t x = halves_from(w, t0, t1, 4 * B);
-                f[k][0] = field<B, 0>(x);
-                f[k][1] = field<B, 1>(x);
-                f[k][2] = field<B, 2 % Fld<B>::N>(x);
-                f[k][3] = field<B, 3 % Fld<B>::N>(x);
+                f[g][k][0] = field<B, 0>(x);
+                f[g][k][1] = field<B, 1>(x);
+                f[g][k][2] = field<B, 2 % Fld<B>::N>(x);
+                f[g][k][3] = field<B, 3 % Fld<B>::N>(x);
             } else {
                 const uint32_t x = halves_from(w, t0, t1, 2 * B), y = halves_from(w, t0 + 2 * B, t1 + 2 * B, 2 * B);
-                f[k][0] = field<B, 0>(x);
-                f[k][1] = field<B, 1>(x);
-                f[k][2] = field<B, 0>(y);
-                f[k][3] = field<B, 1>(y);
+                f[g][k][0] = field<B, 0>(x);
+                f[g][k][1] = field<B, 1>(x);
+                f[g][k][2] = field<B, 0>(y);
+                f[g][k][3] = field<B, 1>(y);
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                f[k][i] = h2_bits(__hsub2(bits_h2(f[k][i]), bits_h2(Fld<B>::zero(i % Fld<B>::N))));
+                f[g][k][i] = h2_bits(__hsub2(bits_h2(f[g][k][i]), bits_h2(Fld<B>::zero(i % Fld<B>::N))));
         }
+    }
+}
+
+// acc += (codes of V) x (weights): half a tile.  scales: of the tile; p[nt][k]: weights
+// of tokens 16 half + 8 k + 2 j + {0, 1} for row n = lane / 4.
+template <int D, int NT, bool Masked>
+QG_DEV void v_product(const uint8_t* scales, int half, int lane, const uint32_t (&f)[D / 32][2][4],
+                      const uint32_t (&p)[NT][2], float (&acc)[NT][D / 16][4]) {
+    constexpr int G = D / 32;
+    scales += ((lane & 3) * G * 8 + 4 * half) * 2;
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+        const uint2 su = *reinterpret_cast<const uint2*>(scales + g * 16);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            mma_f16(acc[nt][2 * g], f[0][0], f[0][1], f[1][0], f[1][1], b0[nt], b1[nt]);
-            mma_f16(acc[nt][2 * g + 1], f[0][2], f[0][3], f[1][2], f[1][3], b0[nt], b1[nt]);
+            uint32_t b0 = h2_bits(__hmul2(bits_h2(p[nt][0]), bits_h2(su.x)));
+            uint32_t b1 = h2_bits(__hmul2(bits_h2(p[nt][1]), bits_h2(su.y)));
+            if constexpr (Masked) {  // a weight of 0 is 0 whatever the scale it meets
+                b0 &= __hneu2_mask(bits_h2(p[nt][0]), bits_h2(0));
+                b1 &= __hneu2_mask(bits_h2(p[nt][1]), bits_h2(0));
+            }
+            mma_f16(acc[nt][2 * g], f[g][0][0], f[g][0][1], f[g][1][0], f[g][1][1], b0, b1);
+            mma_f16(acc[nt][2 * g + 1], f[g][0][2], f[g][0][3], f[g][1][2], f[g][1][3], b0, b1);
         }
     }
 }
 
 template <int D, int NT, int B, bool Masked>
 QG_DEV void output_tile(const uint8_t* part, int lane, const uint32_t (&p)[2][NT][2], float (&acc)[NT][D / 16][4]) {
-    output_half<D, NT, B, Masked>(part, 0, lane, p[0], acc);
-    output_half<D, NT, B, Masked>(part, 1, lane, p[1], acc);
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        uint32_t f[D / 32][2][4];
+        v_fields<D, B>(part, half, lane, f);
+        v_product<D, NT, Masked>(part + 4 * D * B, half, lane, f, p[half], acc);
+    }
 }
 
 // largest V scale among this lane's share of the tile's, up to token slot `last`
@@ -656,9 +665,11 @@ QG_DEV void att_seek(const KvAttend& a, const long long* prefix, int nthreads, i
     c.rb = (int)(item - (long long)c.h * c.s.nrb);
 }
 
-// the next tile; `more`: there is one
+// the next tile, number `at` of the call, if there is one (`more`); sequences without
+// rows are passed over by a new search
 template <int RB>
-QG_DEV void att_next(const KvAttend& a, AttCursor& c, bool more) {
+QG_DEV void att_next(const KvAttend& a, const long long* prefix, int nthreads, int chunk, AttCursor& c, bool more,
+                     long long at) {
     if (++c.tile < c.s.tiles) return;
     c.tile = 0;
     if (++c.rb < c.s.nrb) return;
@@ -666,10 +677,9 @@ QG_DEV void att_next(const KvAttend& a, AttCursor& c, bool more) {
     if (++c.h < a.pg.heads) return;
     c.h = 0;
     if (!more || c.b + 1 >= a.bt.num_seqs) return;
-    do {
-        ++c.b;
-        c.s = att_seq<RB>(a, c.b);
-    } while (c.s.nrb == 0 && c.b + 1 < a.bt.num_seqs);
+    ++c.b;
+    c.s = att_seq<RB>(a, c.b);
+    if (c.s.nrb == 0) att_seek<RB>(a, prefix, nthreads, chunk, at, c);
 }
 
 // rotate back, divide and store one row held by a warp (E consecutive dims a lane);
@@ -744,14 +754,15 @@ __global__ void __launch_bounds__(AttCfg<D, NT>::T, 1) kv_attend_kernel(KvAttend
     }
     prefix[threadIdx.x] = before + inc - mine;
     __syncthreads();
-    // two tiles a warp at least: a join across CTAs costs more than a second tile
-    const long long share = max(div_ll(total + gridDim.x - 1, gridDim.x), 2ll * W);
+    // 16 tiles a CTA at least: a join across CTAs costs more than two tiles a warp
+    const long long share = max(div_ll(total + gridDim.x - 1, gridDim.x), 16ll);
     const long long cta0 = min(share * blockIdx.x, total), cta1 = min(cta0 + share, total);
     if (cta0 >= cta1) return;
     // warp w's first tile: shares differ by one at most
     const int cta_tiles = (int)(cta1 - cta0);
     const long long w0 = cta0 + (cta_tiles / W) * warp + min(warp, cta_tiles % W);
     int count = cta_tiles / W + (warp < cta_tiles % W ? 1 : 0);
+    const long long w_end = w0 + count;
 
     // ---- Walk the CTA's first items.  Where it has no more than QN all warps share their
     // rotated queries: each warp fetches some of the rows here, ahead of the cache's tiles,
@@ -800,7 +811,7 @@ __global__ void __launch_bounds__(AttCfg<D, NT>::T, 1) kv_attend_kernel(KvAttend
             if (w0 >= at) my_item = items;
             at += c.s.tiles;
             c.tile = c.s.tiles - 1;
-            att_next<RB>(a, c, at < cta1);
+            att_next<RB>(a, prefix, T, chunk, c, at < cta1, at);
         }
     }
     const bool shared_q = items <= C::QN;
@@ -834,7 +845,7 @@ __global__ void __launch_bounds__(AttCfg<D, NT>::T, 1) kv_attend_kernel(KvAttend
         ++pc.tile;
         if (--page_left == 0 && pc.tile == pc.s.tiles) {
             --pc.tile;
-            att_next<RB>(a, pc, left > 0);
+            att_next<RB>(a, prefix, T, chunk, pc, left > 0, w_end - left);
         }
     };
     for (int i = 0; i < a.stages && left > 0; ++i) issue(i);
@@ -1135,7 +1146,7 @@ __global__ void __launch_bounds__(AttCfg<D, NT>::T, 1) kv_attend_kernel(KvAttend
         at += n_tiles;
         count -= n_tiles;
         cc.tile = cs.tiles - 1;
-        att_next<RB>(a, cc, count > 0);
+        att_next<RB>(a, prefix, T, chunk, cc, count > 0, at);
     }
     if (dead)  // what is still in flight into this warp's ring
         for (int i = 0; i < a.stages; ++i) mbar_wait(&full[i], parity ^ (i < stage ? 1 : 0));

@@ -1371,7 +1371,7 @@ int qgemm_kv_attend(const qgemm_kv_cache* cache, const qgemm_kv_batch* batch, in
         return st;
     a.lse = d_lse;
     a.q_heads = q_heads;
-    a.window = window;
+    a.window = window < (1 << 30) ? window : 0;  // no sequence is longer
     a.scale = scale;
     DeviceInfo* dev = nullptr;
     if ((st = current_device_info(&dev)) != QGEMM_OK) return st;

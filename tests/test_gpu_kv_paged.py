@@ -285,6 +285,104 @@ def test_long_sequence_split(q):
         check_attention(out.double().cpu().numpy(), lse.double().cpu().numpy(), ref, BF16, D, 20011)
 
 
+def test_many_short_and_empty_sequences(q):
+    """More sequences than a CTA has threads, most of them without new rows, some without tokens."""
+    rng = np.random.default_rng(21)
+    B, heads, G, D = 900, 2, 3, 64
+    lens = [int(x) for x in rng.integers(0, 50, B)]
+    news = [int(x) for x in (rng.random(B) < 0.15) * rng.integers(1, 3, B)]
+    s = problem(rng, lens, news, heads, D, 4, 4, 32)
+    cache, batch = to_gpu(q, s, heads)
+    T = int(s.cu[-1])
+    k, v = (values(rng, (T, heads, D), F16) for _ in range(2))
+    q.qgemm_kv_append(*(torch.as_tensor(a).to(F16).cuda() for a in (k, v)), cache, batch)
+    s.append(k.astype(np.float16), v.astype(np.float16))
+    assert np.array_equal(cache.pages.view(torch.uint8).cpu().numpy(), s.pages)
+    qs = values(rng, (T, heads * G, D), F16)
+    out, lse = torch.empty(T, heads * G, D, dtype=F16, device="cuda"), torch.empty(T, heads * G, device="cuda")
+    q.qgemm_kv_attend(torch.as_tensor(qs).to(F16).cuda(), cache, batch, out, q.kv_workspace(cache, heads * G), lse=lse)
+    check_attention(out.double().cpu().numpy(), lse.double().cpu().numpy(), s.attend(qs, heads, D ** -0.5), F16, D, 50)
+    ko, vo = torch.empty(T, heads, D, dtype=F16, device="cuda"), torch.empty(T, heads, D, dtype=F16, device="cuda")
+    q.qgemm_kv_gather(cache, batch, ko, vo)
+    for b in range(B):
+        for i in range(max(0, news[b] - lens[b]), news[b]):
+            u = s.context(b, 1, True)[lens[b] - news[b] + i]
+            check_rotated_back(ko[s.cu[b] + i, 1].double().cpu().numpy()[None], u[None], F16)
+
+
+def test_pages_past_four_gigabytes(q):
+    """Offsets in the pool beyond 32 bits: a sequence's pages at its end."""
+    rng = np.random.default_rng(22)
+    heads, G, D, page, n = 8, 4, 128, 512, 1100
+    words = q.qgemm_kv_page_words(heads, D, 8, 8, page)
+    P = (5 << 30) // (4 * words)
+    cache = q.KVCache(torch.zeros(P, words, dtype=torch.int32, device="cuda"), page, heads, D, 8, 8)
+    batch = q.KVBatch(i32([[P - 1, 0, P - 2]]), i32([n]), i32([0, n]))
+    k, v = (torch.as_tensor(values(rng, (n, heads, D), F16)).to(F16).cuda() for _ in range(2))
+    q.qgemm_kv_append(k, v, cache, batch)
+    ko, vo = torch.empty_like(k), torch.empty_like(v)
+    q.qgemm_kv_gather(cache, batch, ko, vo)
+    # 8 bits: within half a step of the group's scale in the rotated domain, sqrt(D) of them at most back
+    for x, y in ((k, ko), (v, vo)):
+        err = (x.double() - y.double()).norm(dim=-1)
+        step = x.double().norm(dim=-1) * math.sqrt(D) / 127     # a scale is max |u| / 127 <= |H x| / 127
+        assert (err <= step * math.sqrt(D) / 2 / math.sqrt(D) * 1.05 + 1e-3).all()
+    small = q.KVCache.zeros(3, page, heads, D, 8, 8)            # the same tokens near the start
+    near = q.KVBatch(i32([[2, 0, 1]]), i32([n]), i32([0, n]))
+    q.qgemm_kv_append(k, v, small, near)
+    qd = torch.as_tensor(values(rng, (1, heads * G, D), F16)).to(F16).cuda()
+    outs = []
+    for c, table in ((cache, [[P - 1, 0, P - 2]]), (small, [[2, 0, 1]])):
+        o = torch.empty(1, heads * G, D, dtype=F16, device="cuda")
+        q.qgemm_kv_attend(qd, c, q.KVBatch(i32(table), i32([n]), i32([0, 1])), o, q.kv_workspace(c, heads * G))
+        outs.append(o)
+    assert torch.equal(*outs)
+
+
+def test_strided_and_expanded_operands(q):
+    """out as [heads, rows, D] seen from the side, one query expanded over all rows, a large page."""
+    rng = np.random.default_rng(23)
+    heads, G, D, page = 2, 4, 128, 1024
+    lens, news = [1500, 70], [3, 2]
+    s = problem(rng, lens, news, heads, D, 4, 4, page)
+    cache, batch = to_gpu(q, s, heads)
+    qs = values(rng, (1, heads * G, D), BF16)
+    qd = torch.as_tensor(qs).to(BF16).cuda().expand(5, -1, -1)
+    out = torch.empty(heads * G, 5, D, dtype=BF16, device="cuda")
+    lse = torch.empty(5, heads * G, device="cuda")
+    q.qgemm_kv_attend(qd, cache, batch, out.transpose(0, 1), q.kv_workspace(cache, heads * G), lse=lse,
+                      window=(1 << 31) - 1)
+    ref = s.attend(np.repeat(qs, 5, axis=0), heads, D ** -0.5)
+    check_attention(out.transpose(0, 1).double().cpu().numpy(), lse.double().cpu().numpy(), ref, BF16, D, 1500)
+
+
+def test_tiny_and_huge_values(q):
+    """Values near the ends of the types' ranges: scales of V far below and above 1, scores that differ by a lot."""
+    rng = np.random.default_rng(24)
+    heads, G, D = 2, 8, 128
+    for exponent in (-13, -6, 8):
+        s = problem(rng, [300, 33], [1, 1], heads, D, 4, 4, 64)
+        c = R.parts(D, 4, 4)
+        sc = s.pages[..., c[3]:c[3] + 2 * D].view(np.float16)
+        finite = np.isfinite(sc)
+        sc[finite] = (sc[finite].astype(np.float64) * 2.0 ** exponent).astype(np.float16)
+        cache, batch = to_gpu(q, s, heads)
+        qs = values(rng, (2, heads * G, D), BF16) * 2.0 ** -20
+        out, lse = torch.empty(2, heads * G, D, dtype=BF16, device="cuda"), torch.empty(2, heads * G, device="cuda")
+        scale = 2.0 ** 20 * D ** -0.5
+        q.qgemm_kv_attend(torch.as_tensor(qs).to(BF16).cuda(), cache, batch, out, q.kv_workspace(cache, heads * G),
+                          scale=scale, lse=lse)
+        o, e, mass, score = s.attend(qs, heads, scale)
+        got = out.double().cpu().numpy()
+        # weight times scale is fp16: below 2^-14 in steps of 2^-24 next to weights of 2^10 and more, so each of
+        # the 300 tokens may add 2^-35 of a code of 8 to the relative terms of check_attention
+        extra = 300 * 2.0 ** -35 * 8 * math.sqrt(D)
+        ds = score * (2.0 ** -22 + (D + 32) * U32)
+        tol = (mass * (2.0 ** -10 + 2 * ds + 2.0 ** -18 + 8 * 300 * U32))[..., None] * 1.01
+        tol = tol + np.abs(o) * torch.finfo(BF16).eps / 2 * 1.01 + extra
+        assert (np.abs(got - o) <= tol).all(), float((np.abs(got - o) / tol).max())
+
+
 def test_decoding_loop(q):
     """A prompt written in uneven chunks, then tokens one by one with a captured append + attend that is replayed
     as the lengths grow across pages: every step against 64 bits."""
@@ -382,6 +480,22 @@ def test_not_a_number_stays_in_its_row(q):
     ref = s.attend(qs, heads, D ** -0.5)
     keep = ~bad
     check_attention(o[keep][None], e[keep][None], tuple(r[keep][None] for r in ref), F16, D, 200)
+    # a NaN token behind a row's position, or before its window, does not reach it
+    s = problem(rng, [200], [3], heads, D, 4, 4, 64)
+    for pos, part in ((199, c[3]), (199, c[1]), (150, c[3])):
+        p, tile, slot = s.place(0, pos)
+        key = part == c[1]
+        s.pages[p, :, tile, part:part + 2 * D].view(np.uint16)[:, R.scale_places(D, key)[slot]] = 0x7e00
+    cache, batch = to_gpu(q, s, heads)
+    qs = values(rng, (3, heads * G, D), F16)
+    out, lse = torch.empty(3, heads * G, D, dtype=F16, device="cuda"), torch.empty(3, heads * G, device="cuda")
+    q.qgemm_kv_attend(torch.as_tensor(qs).to(F16).cuda(), cache, batch, out, q.kv_workspace(cache, heads * G), lse=lse,
+                      window=40)
+    with np.errstate(invalid="ignore"):
+        ref = s.attend(qs, heads, D ** -0.5, 40)
+    check_attention(out[:2].double().cpu().numpy(), lse[:2].double().cpu().numpy(), tuple(r[:2] for r in ref), F16, D,
+                    200)
+    assert torch.isnan(out[2]).all() and torch.isnan(lse[2]).all()
 
 
 def test_positions_without_a_page_are_refused(q):
