@@ -53,6 +53,7 @@ struct KvAttend {
 };
 
 constexpr int kAttMaxStages = 8;
+constexpr int kAttLowest = -14;       // V scales below 2^-13 count as if they were that
 constexpr float kAttNone = -3.4e38f;  // the weights' offset before any token: below every finite score
 
 template <int D, int NT>
@@ -551,24 +552,32 @@ QG_DEV void v_fields(const uint8_t* part, int half, int lane, uint32_t (&f)[D / 
     }
 }
 
-// acc += (codes of V) x (weights): half a tile.  scales: of the tile; p[nt][k]: weights
-// of tokens 16 half + 8 k + 2 j + {0, 1} for row n = lane / 4.
+// acc += (codes of V) x (weights times scales): half a tile.  w[nt][c]: the weight of
+// token 16 half + 8 (c / 2) + r for row 8 nt + 2 j + c % 2.  The product with the
+// group's scale is taken in fp32 and rounded once, to the fp16 of the B operand;
+// movmatrix turns it from [token][row] to [row][token].
 template <int D, int NT, bool Masked>
 QG_DEV void v_product(const uint8_t* scales, int half, int lane, const uint32_t (&f)[D / 32][2][4],
-                      const uint32_t (&p)[NT][2], float (&acc)[NT][D / 16][4]) {
+                      const float (&w)[NT][4], float (&acc)[NT][D / 16][4]) {
     constexpr int G = D / 32;
-    scales += ((lane & 3) * G * 8 + 4 * half) * 2;
+    const int r = lane >> 2;
+    const uint32_t pick = (r & 1) ? 0x7632u : 0x5410u;  // u of token 8 tt + r
+    scales += ((r >> 1) * G * 8 + 4 * half) * 2;
 #pragma unroll
     for (int g = 0; g < G; ++g) {
         const uint2 su = *reinterpret_cast<const uint2*>(scales + g * 16);
+        const __half2 sh = bits_h2(__byte_perm(su.x, su.y, pick));
+        const float s0 = __low2float(sh), s1 = __high2float(sh);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            uint32_t b0 = h2_bits(__hmul2(bits_h2(p[nt][0]), bits_h2(su.x)));
-            uint32_t b1 = h2_bits(__hmul2(bits_h2(p[nt][1]), bits_h2(su.y)));
-            if constexpr (Masked) {  // a weight of 0 is 0 whatever the scale it meets
-                b0 &= __hneu2_mask(bits_h2(p[nt][0]), bits_h2(0));
-                b1 &= __hneu2_mask(bits_h2(p[nt][1]), bits_h2(0));
+            float b[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                b[c] = w[nt][c] * (c < 2 ? s0 : s1);
+                if constexpr (Masked) b[c] = w[nt][c] == 0.f ? 0.f : b[c];  // whatever the scale it meets
             }
+            const uint32_t b0 = movm_trans(h2_bits(__floats2half2_rn(b[0], b[1])));
+            const uint32_t b1 = movm_trans(h2_bits(__floats2half2_rn(b[2], b[3])));
             mma_f16(acc[nt][2 * g], f[g][0][0], f[g][0][1], f[g][1][0], f[g][1][1], b0, b1);
             mma_f16(acc[nt][2 * g + 1], f[g][0][2], f[g][0][3], f[g][1][2], f[g][1][3], b0, b1);
         }
@@ -576,12 +585,12 @@ QG_DEV void v_product(const uint8_t* scales, int half, int lane, const uint32_t 
 }
 
 template <int D, int NT, int B, bool Masked>
-QG_DEV void output_tile(const uint8_t* part, int lane, const uint32_t (&p)[2][NT][2], float (&acc)[NT][D / 16][4]) {
+QG_DEV void output_tile(const uint8_t* part, int lane, const float (&w)[2][NT][4], float (&acc)[NT][D / 16][4]) {
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
         uint32_t f[D / 32][2][4];
         v_fields<D, B>(part, half, lane, f);
-        v_product<D, NT, Masked>(part + 4 * D * B, half, lane, f, p[half], acc);
+        v_product<D, NT, Masked>(part + 4 * D * B, half, lane, f, w[half], acc);
     }
 }
 
@@ -878,7 +887,7 @@ __global__ void __launch_bounds__(AttCfg<D, NT>::T, 1) kv_attend_kernel(KvAttend
         // tiles [u0, u1) of these are seen whole by every row
         const int t_base = (cs.t0 + cc.tile) * kTileTokens;
         const int u1 = (lo_pos + 1 - t_base) >> 5, u0 = a.window > 0 ? ((hi_pos - a.window - t_base) >> 5) + 1 : 0;
-        int qpos[NT][2], ve = 0;  // ve: exponent of the largest V scale, 0 at least
+        int qpos[NT][2], ve = kAttLowest;  // ve: exponent of the largest V scale seen
         float limit[NT][2];       // a score may reach this before mo moves
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -991,29 +1000,26 @@ __global__ void __launch_bounds__(AttCfg<D, NT>::T, 1) kv_attend_kernel(KvAttend
                     ve = vn;
                     weigh();
                 }
-                uint32_t p[2][NT][2];
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
                         l[nt][0] += w[h][nt][0] + w[h][nt][2];
                         l[nt][1] += w[h][nt][1] + w[h][nt][3];
-                        p[h][nt][0] = movm_trans(h2_bits(__floats2half2_rn(w[h][nt][0], w[h][nt][1])));
-                        p[h][nt][1] = movm_trans(h2_bits(__floats2half2_rn(w[h][nt][2], w[h][nt][3])));
                     }
                 if constexpr (VB > 0) {
                     if (masked)
-                        output_tile<D, NT, VB, true>(vpart, lane, p, acc);
+                        output_tile<D, NT, VB, true>(vpart, lane, w, acc);
                     else
-                        output_tile<D, NT, VB, false>(vpart, lane, p, acc);
+                        output_tile<D, NT, VB, false>(vpart, lane, w, acc);
                 } else {
                     switch (a.pg.vb) {
 #define QG_OUTPUT(B)                                               \
     case B:                                                        \
         if (masked)                                                \
-            output_tile<D, NT, B, true>(vpart, lane, p, acc);      \
+            output_tile<D, NT, B, true>(vpart, lane, w, acc);      \
         else                                                       \
-            output_tile<D, NT, B, false>(vpart, lane, p, acc);     \
+            output_tile<D, NT, B, false>(vpart, lane, w, acc);     \
         break;
                         QG_OUTPUT(2)
                         QG_OUTPUT(3)
