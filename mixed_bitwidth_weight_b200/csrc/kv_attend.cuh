@@ -53,6 +53,12 @@ struct KvAttend {
 };
 
 constexpr int kAttMaxStages = 8;
+// The matrix instruction aligns products by their operands' exponents, and a subnormal's is
+// that of 2^-14 whatever its leading zeros: codes of b bits lose up to 10 - b of the sum's 24
+// bits, which leaves a score 5e-6 of its size off at 2 to 4 bits.  The error averages out
+// over the tokens (the lse is 1e-6 off at 300, 4e-7 at 5000).  Rows that see up to kAttFine
+// tokens take their codes as normal numbers, one multiplication (exact) per pair: 3e-7.
+constexpr int kAttFine = 2048;
 constexpr int kAttLowest = -14;       // V scales below 2^-13 count as if they were that
 constexpr float kAttNone = -3.4e38f;  // the weights' offset before any token: below every finite score
 
@@ -141,8 +147,12 @@ struct Fld {
     static constexpr uint32_t mask(int i) {
         return (B == 4 && (i & 1) ? 0xffu : ((1u << B) - 1u) << at(i)) * 0x10001u;
     }
-    static constexpr uint32_t zero(int i) {
-        return (B == 4 && (i & 1) ? 0x88u : (1u << (B - 1)) << at(i)) * 0x10001u;
+    // -z in the field's place times 2^10, as a pair of normal fp16 numbers
+    static constexpr uint32_t minus_zero(int i) {
+        const uint32_t v = B == 4 && (i & 1) ? 0x88u : (1u << (B - 1)) << at(i);
+        int e = 0;
+        while ((v >> e) > 1) ++e;
+        return (0x8000u | (uint32_t)(e + 1) << 10 | (v - (1u << e)) << (10 - e)) * 0x10001u;
     }
 };
 
@@ -279,7 +289,8 @@ QG_DEV void k_fragment(const uint32_t (&w)[D * B / 64], int g, int step, uint32_
 // Scores of a tile, s[half][nt][c].  The four dependent matrix instructions of a
 // group are issued a step at a time over all groups, so that eight chains (four
 // with 64 dims) hide each other's latency.
-template <int D, int NT, int B>
+// Fine: the codes made normal numbers, times 2^10 (see kAttFine).
+template <int D, int NT, int B, bool Fine>
 QG_DEV void scores_tile(const uint8_t* rec, int lane, const AttQ<D, NT>& q, float (&s)[2][NT][4]) {
     constexpr int G = D / 32, NW = D * B / 64, HB = D * NT > 128 ? 1 : 2;  // halves at a time
 #pragma unroll
@@ -315,6 +326,9 @@ QG_DEV void scores_tile(const uint8_t* rec, int lane, const AttQ<D, NT>& q, floa
                 for (int g = 0; g < G; ++g) {
                     uint32_t(&x)[4] = a[h][g];
                     k_fragment<D, B>(w[h], g, step, x);
+                    if constexpr (Fine)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) x[i] = h2_bits(__hmul2(bits_h2(x[i]), bits_h2(0x64006400u)));
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
                         if (step == 0)
@@ -519,7 +533,8 @@ QG_DEV void load_queries(const float* area, int lane, AttQ<D, NT>& q) {
 }
 
 // ------------------------------------------------------------------- output
-// A registers of half a tile's V codes, c - z, in units of their fields: f[g][k][i]
+// A registers of half a tile's V codes, (c - z) 2^-14 in units of their fields, one exact
+// fused multiply-add a pair (which also makes them normal numbers, see kAttFine): f[g][k][i]
 // holds field i of group g's dims for tokens 16 half + 8 k + 2 j + {0, 1}.
 template <int D, int B>
 QG_DEV void v_fields(const uint8_t* part, int half, int lane, uint32_t (&f)[D / 32][2][4]) {
@@ -547,7 +562,8 @@ QG_DEV void v_fields(const uint8_t* part, int half, int lane, uint32_t (&f)[D / 
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                f[g][k][i] = h2_bits(__hsub2(bits_h2(f[g][k][i]), bits_h2(Fld<B>::zero(i % Fld<B>::N))));
+                f[g][k][i] = h2_bits(__hfma2(bits_h2(f[g][k][i]), bits_h2(0x64006400u),
+                                             bits_h2(Fld<B>::minus_zero(i % Fld<B>::N))));
         }
     }
 }
@@ -882,6 +898,17 @@ __global__ void __launch_bounds__(AttCfg<D, NT>::T, 1) kv_attend_kernel(KvAttend
         else
             rotate_queries<D, NT>(a, cs.row0, rows, r_base, cc.h, lane, q);
         ++my_item;
+        const bool fine = a.pg.kb <= 5 && cs.tiles <= kAttFine / kTileTokens;
+        if (fine)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+                for (int g = 0; g < G; ++g)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) q.zq[nt][g][c] *= 1024.f;
+                q.f[nt][0] *= 1.f / 1024.f;
+                q.f[nt][1] *= 1.f / 1024.f;
+            }
         const int lo_pos = cs.pos0 + r_base / a.group;
         const int hi_pos = cs.pos0 + (min(r_base + RB, rows) - 1) / a.group;
         // tiles [u0, u1) of these are seen whole by every row
@@ -912,21 +939,35 @@ __global__ void __launch_bounds__(AttCfg<D, NT>::T, 1) kv_attend_kernel(KvAttend
             const uint8_t* rec = ring + rec_at;
             const uint8_t* vpart = rec + k_bytes;
             {
-                if constexpr (KB > 0) {
-                    scores_tile<D, NT, KB>(rec, lane, q, s);
+                if constexpr (KB > 5) {
+                    scores_tile<D, NT, KB, false>(rec, lane, q, s);
+                } else if constexpr (KB > 0) {
+                    if (fine)
+                        scores_tile<D, NT, KB, true>(rec, lane, q, s);
+                    else
+                        scores_tile<D, NT, KB, false>(rec, lane, q, s);
                 } else {
-                    switch (a.pg.kb) {
-#define QG_SCORES(B)                            \
-    case B:                                     \
-        scores_tile<D, NT, B>(rec, lane, q, s); \
+                    switch (fine ? a.pg.kb + 8 : a.pg.kb) {
+#define QG_SCORES(B)                                   \
+    case B:                                            \
+        scores_tile<D, NT, B, false>(rec, lane, q, s); \
         break;
-                    QG_SCORES(2)
-                    QG_SCORES(3)
-                    QG_SCORES(4)
-                    QG_SCORES(5)
-                    QG_SCORES(6)
-                    QG_SCORES(8)
+#define QG_SCORES_FINE(B)                             \
+    case B + 8:                                       \
+        scores_tile<D, NT, B, true>(rec, lane, q, s); \
+        break;
+                        QG_SCORES(2)
+                        QG_SCORES(3)
+                        QG_SCORES(4)
+                        QG_SCORES(5)
+                        QG_SCORES(6)
+                        QG_SCORES(8)
+                        QG_SCORES_FINE(2)
+                        QG_SCORES_FINE(3)
+                        QG_SCORES_FINE(4)
+                        QG_SCORES_FINE(5)
 #undef QG_SCORES
+#undef QG_SCORES_FINE
                     }
                 }
             }
@@ -1052,8 +1093,8 @@ __global__ void __launch_bounds__(AttCfg<D, NT>::T, 1) kv_attend_kernel(KvAttend
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     float &u = acc[nt][i][c], &v = acc[nt][i][c + 2];  // fields 2 (i % 2) and the next
-                    u *= __uint_as_float((uint32_t)(127 + 24 - field_at(a.pg.vb, 2 * (i & 1))) << 23);
-                    v *= __uint_as_float((uint32_t)(127 + 24 - field_at(a.pg.vb, 2 * (i & 1) + 1)) << 23);
+                    u *= __uint_as_float((uint32_t)(127 + 14 - field_at(a.pg.vb, 2 * (i & 1))) << 23);
+                    v *= __uint_as_float((uint32_t)(127 + 14 - field_at(a.pg.vb, 2 * (i & 1) + 1)) << 23);
                     if (a.pg.vb == 4) v -= u * 0.0625f;
                 }
 #pragma unroll
