@@ -251,12 +251,15 @@ struct AttQ {
     float zq[NT][D / 32][4];  // an accumulator's four: rows r and r + 8 start alike
     float f[NT][2];  // factor of a score, log2 units
     // the accumulators' C operand is four consecutive registers: without the moves that the compiler
-    // cannot see through it keeps two and copies them before each use
+    // cannot see through it keeps two and copies them before each use (which it is left to do where
+    // the registers for four are not there)
     QG_DEV void set_zero(int nt, int g, float x, float y) {
-        zq[nt][g][0] = x;
-        zq[nt][g][1] = y;
-        asm volatile("mov.b32 %0, %1;" : "=f"(zq[nt][g][2]) : "f"(x));
-        asm volatile("mov.b32 %0, %1;" : "=f"(zq[nt][g][3]) : "f"(y));
+        zq[nt][g][0] = zq[nt][g][2] = x;
+        zq[nt][g][1] = zq[nt][g][3] = y;
+        if constexpr (D * NT <= 128) {
+            asm volatile("mov.b32 %0, %1;" : "=f"(zq[nt][g][2]) : "f"(x));
+            asm volatile("mov.b32 %0, %1;" : "=f"(zq[nt][g][3]) : "f"(y));
+        }
     }
 };
 
@@ -742,6 +745,7 @@ __global__ void __launch_bounds__(AttCfg<D, NT>::T, 1) kv_attend_kernel(KvAttend
     constexpr int W = C::W, G = C::G, RB = C::RB, E = D / 32, T = C::T;
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ long long sh_total[W];
+    __shared__ uint32_t sh_items[W];
     __shared__ int sh_last[2];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int rec_bytes = kv_record_bytes<D>(a.pg.kb, a.pg.vb), k_bytes = 4 * D * a.pg.kb + 2 * D;
@@ -755,10 +759,11 @@ __global__ void __launch_bounds__(AttCfg<D, NT>::T, 1) kv_attend_kernel(KvAttend
 
     // ---- the call's work, this CTA's and each warp's share
     const int chunk = (a.bt.num_seqs + T - 1) / T;
-    long long mine = 0;
+    long long mine = 0, mine_items = 0;
     for (int b = threadIdx.x * chunk; b < min((int)(threadIdx.x + 1) * chunk, a.bt.num_seqs); ++b) {
         const AttSeq s = att_seq<RB>(a, b);
         mine += (long long)s.nrb * a.pg.heads * s.tiles;
+        mine_items += (long long)s.nrb * a.pg.heads;
     }
     long long inc = mine;
 #pragma unroll
@@ -766,21 +771,29 @@ __global__ void __launch_bounds__(AttCfg<D, NT>::T, 1) kv_attend_kernel(KvAttend
         const long long v = __shfl_up_sync(0xffffffffu, inc, o);
         if (lane >= o) inc += v;
     }
-    if (lane == 31) sh_total[warp] = inc;
+    // (items are only averaged over: a count that saturates does)
+    const uint32_t warp_items = __reduce_add_sync(0xffffffffu, (uint32_t)min(mine_items, 1ll << 21));
+    if (lane == 31) {
+        sh_total[warp] = inc;
+        sh_items[warp] = warp_items;
+    }
     if (lane < kAttMaxStages) mbar_init(&full[lane], 1);
     if (threadIdx.x < 2 * W) frags[threadIdx.x].tiles = 0;
     fence_mbar_init();
     __syncthreads();
-    long long before = 0, total = 0;
+    long long before = 0, total = 0, total_items = 0;
 #pragma unroll
     for (int w = 0; w < W; ++w) {
         if (w < warp) before += sh_total[w];
         total += sh_total[w];
+        total_items += sh_items[w];
     }
     prefix[threadIdx.x] = before + inc - mine;
     __syncthreads();
-    // 16 tiles a CTA at least: a join across CTAs costs more than two tiles a warp
-    const long long share = max(div_ll(total + gridDim.x - 1, gridDim.x), 16ll);
+    // An average item's tiles a CTA at least, up to 16 of them: a join across CTAs costs more
+    // than two tiles a warp
+    const long long share =
+        max(div_ll(total + gridDim.x - 1, gridDim.x), min(div_ll(total + total_items - 1, max((int)total_items, 1)), 16ll));
     const long long cta0 = min(share * blockIdx.x, total), cta1 = min(cta0 + share, total);
     if (cta0 >= cta1) return;
     // warp w's first tile: shares differ by one at most
