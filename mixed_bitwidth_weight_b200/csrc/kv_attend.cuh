@@ -62,21 +62,21 @@ constexpr int kAttFine = 2048;
 constexpr int kAttLowest = -14;       // V scales below 2^-13 count as if they were that
 constexpr float kAttNone = -3.4e38f;  // the weights' offset before any token: below every finite score
 
-template <int D, int NT>
+template <int D>
 struct AttCfg {
-    static constexpr int W = D * NT <= 64 ? 12 : 8;   // warps: 168 registers a thread with 12, 255 with 8
+    static constexpr int W = D <= 64 ? 12 : 8;   // warps: 168 registers a thread with 12, 255 with 8
     static constexpr int T = 32 * W;
     static constexpr int G = D / 32;
-    static constexpr int RB = 8 * NT;                 // query rows of an item
+    static constexpr int RB = 8;                      // query rows of an item: the N of the matrix instruction
     static constexpr int OS = D + 4;                  // row stride of a slot: conflict-free float4 stores
     static constexpr int SlotFloats = RB * OS + 2 * RB;
     static constexpr int SlotBytes = SlotFloats * 4;
     static constexpr int GSlot = RB * D + 2 * RB;     // floats of a global slot
-    // an item's rotated query: [nt][g][hi, lo][lane] 16 bytes, then zq [nt][g][8], f [nt][8];
+    // an item's rotated query: [g][hi, lo][lane] 16 bytes, then zq [g][8], f [8];
     // QN of them are shared by the CTA's warps
-    static constexpr int QN = D * NT <= 128 ? 6 : 4;
-    static constexpr int QZero = NT * G * 256, QFactor = QZero + NT * G * 8;
-    static constexpr int QFloats = QFactor + NT * 8, QBytes = QFloats * 4;
+    static constexpr int QN = D <= 128 ? 6 : 4;
+    static constexpr int QZero = G * 256, QFactor = QZero + G * 8;
+    static constexpr int QFloats = QFactor + 8, QBytes = QFloats * 4;
     // shared memory: slots, query areas, barriers, fragments, prefix sums, rings
     static constexpr int QAt = W * SlotBytes;
     static constexpr int BarAt = (QAt + QN * QBytes + 15) / 16 * 16;
@@ -245,20 +245,20 @@ QG_DEV void load_words(const uint8_t* part, int half, int lane, uint32_t (&w)[D 
 // ------------------------------------------------------------------- scores
 // The query rows of an item in the B operand's layout: hi and lo parts, per
 // group and k step two registers, and -z 2^-24 times their sums.
-template <int D, int NT>
+template <int D>
 struct AttQ {
-    uint32_t hi[NT][D / 32][4], lo[NT][D / 32][4];
-    float zq[NT][D / 32][4];  // an accumulator's four: rows r and r + 8 start alike
-    float f[NT][2];  // factor of a score, log2 units
+    uint32_t hi[D / 32][4], lo[D / 32][4];
+    float zq[D / 32][4];  // an accumulator's four: rows r and r + 8 start alike
+    float f[2];  // factor of a score, log2 units
     // the accumulators' C operand is four consecutive registers: without the moves that the compiler
     // cannot see through it keeps two and copies them before each use (which it is left to do where
     // the registers for four are not there)
-    QG_DEV void set_zero(int nt, int g, float x, float y) {
-        zq[nt][g][0] = zq[nt][g][2] = x;
-        zq[nt][g][1] = zq[nt][g][3] = y;
-        if constexpr (D * NT <= 128) {
-            asm volatile("mov.b32 %0, %1;" : "=f"(zq[nt][g][2]) : "f"(x));
-            asm volatile("mov.b32 %0, %1;" : "=f"(zq[nt][g][3]) : "f"(y));
+    QG_DEV void set_zero(int g, float x, float y) {
+        zq[g][0] = zq[g][2] = x;
+        zq[g][1] = zq[g][3] = y;
+        if constexpr (D <= 128) {
+            asm volatile("mov.b32 %0, %1;" : "=f"(zq[g][2]) : "f"(x));
+            asm volatile("mov.b32 %0, %1;" : "=f"(zq[g][3]) : "f"(y));
         }
     }
 };
@@ -289,17 +289,17 @@ QG_DEV void k_fragment(const uint32_t (&w)[D * B / 64], int g, int step, uint32_
     }
 }
 
-// Scores of a tile, s[half][nt][c].  The four dependent matrix instructions of a
+// Scores of a tile, s[half][c].  The four dependent matrix instructions of a
 // group are issued a step at a time over all groups, so that eight chains (four
 // with 64 dims) hide each other's latency.
 // Fine: the codes made normal numbers, times 2^10 (see kAttFine).
-template <int D, int NT, int B, bool Fine>
-QG_DEV void scores_tile(const uint8_t* rec, int lane, const AttQ<D, NT>& q, float (&s)[2][NT][4]) {
-    constexpr int G = D / 32, NW = D * B / 64, HB = D * NT > 128 ? 1 : 2;  // halves at a time
+template <int D, int B, bool Fine>
+QG_DEV void scores_tile(const uint8_t* rec, int lane, const AttQ<D>& q, float (&s)[2][4]) {
+    constexpr int G = D / 32, NW = D * B / 64, HB = D > 128 ? 1 : 2;  // halves at a time
 #pragma unroll
     for (int h0 = 0; h0 < 2; h0 += HB) {
         uint32_t w[HB][NW], sc[HB][G];
-        float c[HB][NT][G][4];
+        float c[HB][G][4];
 #pragma unroll
         for (int h = 0; h < HB; ++h) {
             load_words<D, B>(rec, h0 + h, lane, w[h]);
@@ -332,23 +332,17 @@ QG_DEV void scores_tile(const uint8_t* rec, int lane, const AttQ<D, NT>& q, floa
                     if constexpr (Fine)
 #pragma unroll
                         for (int i = 0; i < 4; ++i) x[i] = h2_bits(__hmul2(bits_h2(x[i]), bits_h2(0x64006400u)));
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        if (step == 0)
-                            mma_f16_from(c[h][nt][g], x[0], x[1], x[2], x[3], q.hi[nt][g][0], q.hi[nt][g][1],
-                                         q.zq[nt][g]);
-                        else
-                            mma_f16(c[h][nt][g], x[0], x[1], x[2], x[3], q.hi[nt][g][2], q.hi[nt][g][3]);
-                    }
+                    if (step == 0)
+                        mma_f16_from(c[h][g], x[0], x[1], x[2], x[3], q.hi[g][0], q.hi[g][1], q.zq[g]);
+                    else
+                        mma_f16(c[h][g], x[0], x[1], x[2], x[3], q.hi[g][2], q.hi[g][3]);
                 }
 #pragma unroll
             for (int h = 0; h < HB; ++h)
 #pragma unroll
                 for (int g = 0; g < G; ++g)
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-                        mma_f16(c[h][nt][g], a[h][g][0], a[h][g][1], a[h][g][2], a[h][g][3], q.lo[nt][g][2 * step],
-                                q.lo[nt][g][2 * step + 1]);
+                    mma_f16(c[h][g], a[h][g][0], a[h][g][1], a[h][g][2], a[h][g][3], q.lo[g][2 * step],
+                            q.lo[g][2 * step + 1]);
         }
 #pragma unroll
         for (int h = 0; h < HB; ++h)
@@ -358,12 +352,10 @@ QG_DEV void scores_tile(const uint8_t* rec, int lane, const AttQ<D, NT>& q, floa
                 const float s0 = (g & 1) ? __high2float(u0) : __low2float(u0);
                 const float s1 = (g & 1) ? __high2float(u1) : __low2float(u1);
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float si = i < 2 ? s0 : s1, ci = c[h][nt][g][i];
-                        s[h0 + h][nt][i] = g == 0 ? ci * si : fmaf(ci, si, s[h0 + h][nt][i]);
-                    }
+                for (int i = 0; i < 4; ++i) {
+                    const float si = i < 2 ? s0 : s1, ci = c[h][g][i];
+                    s[h0 + h][i] = g == 0 ? ci * si : fmaf(ci, si, s[h0 + h][i]);
+                }
             }
     }
 }
@@ -393,13 +385,13 @@ QG_DEV AttRowScale att_row_scale(const KvAttend& a, float amax) {
     return r;
 }
 
-// Rotate query row n (of 8) of row tile nt, a warp to a row, split it into its two
+// Rotate query row n (of 8), a warp to a row, split it into its two
 // parts and put them where the B operand's lanes read them (row n's dims
 // 32 g + 8 j + i are lane 4 n + j's, pair i % 4, half i / 4).  p: the row in shared memory.
-template <int D, int NT>
-QG_DEV void rotate_query(const KvAttend& a, const uint16_t* p, float* area, int nt, int n, int lane) {
-    using C = AttCfg<D, NT>;
-    constexpr int E = D / 32, G = D / 32;
+template <int D>
+QG_DEV void rotate_query(const KvAttend& a, const uint16_t* p, float* area, int n, int lane) {
+    using C = AttCfg<D>;
+    constexpr int E = D / 32;
     float x[E];
 #pragma unroll
     for (int i = 0; i < E; ++i) x[i] = att_in(a, p[E * lane + i]);
@@ -420,119 +412,113 @@ QG_DEV void rotate_query(const KvAttend& a, const uint16_t* p, float* area, int 
         float vd = v * __uint_as_float((uint32_t)(127 - field_at(a.pg.kb, pair)) << 23);
         if (a.pg.kb == 4 && !(i & 1)) vd = fmaf(x[(i + 1) % E] * rs.up, -0.0625f, vd);
         const __half hi = __float2half_rn(vd), lo = __float2half_rn(vd - __half2float(hi));
-        const int at = ((((nt * G + g) * 2) * 32 + 4 * n + ((d & 31) >> 3)) * 4 + pair) * 2 + ((d >> 2) & 1);
+        const int at = (((g * 2) * 32 + 4 * n + ((d & 31) >> 3)) * 4 + pair) * 2 + ((d >> 2) & 1);
         out[at] = __half_as_ushort(hi);
         out[at + 32 * 8] = __half_as_ushort(lo);
         sum += v;
     }
 #pragma unroll
     for (int o = 1; o < 32 / E; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (lane % (32 / E) == 0) area[C::QZero + (nt * G + g) * 8 + n] = rs.zero * sum;
-    if (lane == 0) area[C::QFactor + nt * 8 + n] = rs.f;
+    if (lane % (32 / E) == 0) area[C::QZero + g * 8 + n] = rs.zero * sum;
+    if (lane == 0) area[C::QFactor + n] = rs.f;
 }
 
 // The same for all rows of an item by one warp for itself, straight into the B
 // operand's registers: lane 4 n + j rotates its share of row n, strides 1, 2, 4 and
 // 32 .. within the lane, 8 and 16 between the four lanes of the row.
-template <int D, int NT>
-QG_DEV void rotate_queries(const KvAttend& a, int row0, int rows, int r_base, int head, int lane, AttQ<D, NT>& q) {
+template <int D>
+QG_DEV void rotate_queries(const KvAttend& a, int row0, int rows, int r_base, int head, int lane, AttQ<D>& q) {
     constexpr int G = D / 32;
+    const int r = r_base + (lane >> 2);
+    float x[G][8];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-        const int r = r_base + nt * 8 + (lane >> 2);
-        float x[G][8];
+    for (int g = 0; g < G; ++g)
 #pragma unroll
-        for (int g = 0; g < G; ++g)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) x[g][i] = 0.f;
-        if (r < rows) {
-            const int tok = r / a.group, hq = head * a.group + (r - tok * a.group);
-            const uint16_t* p = reinterpret_cast<const uint16_t*>(a.q.p) + (row0 + tok) * a.q.row + hq * a.q.head;
-#pragma unroll
-            for (int g = 0; g < G; ++g) {
-                const uint4 u = __ldg(reinterpret_cast<const uint4*>(p + 32 * g + 8 * (lane & 3)));
-                const uint32_t v[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    x[g][i] = att_in(a, (uint16_t)((i & 1) ? v[i / 2] >> 16 : v[i / 2] & 0xffff));
-            }
-        }
-        float amax = 0.f;
-#pragma unroll
-        for (int st = 1; st < D; st <<= 1)
-#pragma unroll
-            for (int g = 0; g < G; ++g)
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    if (st < 8) {
-                        if (i & st) continue;
-                        const float u = x[g][i], v = x[g][i | (st & 7)];
-                        x[g][i] = u + v;
-                        x[g][i | (st & 7)] = u - v;
-                    } else if (st < 32) {
-                        const float o = __shfl_xor_sync(0xffffffffu, x[g][i], st / 8);
-                        x[g][i] = (lane & (st / 8)) ? o - x[g][i] : x[g][i] + o;
-                    } else {
-                        if (g & (st / 32)) continue;
-                        const float u = x[g][i], v = x[(g | (st / 32)) % G][i];
-                        x[g][i] = u + v;
-                        x[(g | (st / 32)) % G][i] = u - v;
-                    }
-                }
-#pragma unroll
-        for (int g = 0; g < G; ++g)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(x[g][i]));
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-        const AttRowScale rs = att_row_scale<D>(a, amax);
-        const int src = (lane & 3) * 8;  // lane of row 2 j
+        for (int i = 0; i < 8; ++i) x[g][i] = 0.f;
+    if (r < rows) {
+        const int tok = r / a.group, hq = head * a.group + (r - tok * a.group);
+        const uint16_t* p = reinterpret_cast<const uint16_t*>(a.q.p) + (row0 + tok) * a.q.row + hq * a.q.head;
 #pragma unroll
         for (int g = 0; g < G; ++g) {
-            float sum = 0.f;
+            const uint4 u = __ldg(reinterpret_cast<const uint4*>(p + 32 * g + 8 * (lane & 3)));
+            const uint32_t v[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float u = x[g][i] * rs.up, v = x[g][i + 4] * rs.up;
-                const float dn = __uint_as_float((uint32_t)(127 - field_at(a.pg.kb, i)) << 23);
-                float ud = u * dn, vd = v * dn;
-                if (a.pg.kb == 4 && !(i & 1)) {
-                    ud = fmaf(x[g][(i + 1) & 3] * rs.up, -0.0625f, ud);
-                    vd = fmaf(x[g][4 + ((i + 1) & 3)] * rs.up, -0.0625f, vd);
-                }
-                const __half2 hi = __floats2half2_rn(ud, vd);
-                q.hi[nt][g][i] = h2_bits(hi);
-                q.lo[nt][g][i] = h2_bits(__floats2half2_rn(ud - __low2float(hi), vd - __high2float(hi)));
-                sum += u + v;
-            }
-            sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-            sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-            sum *= rs.zero;
-            q.set_zero(nt, g, __shfl_sync(0xffffffffu, sum, src), __shfl_sync(0xffffffffu, sum, src + 4));
+            for (int i = 0; i < 8; ++i)
+                x[g][i] = att_in(a, (uint16_t)((i & 1) ? v[i / 2] >> 16 : v[i / 2] & 0xffff));
         }
-        q.f[nt][0] = __shfl_sync(0xffffffffu, rs.f, src);
-        q.f[nt][1] = __shfl_sync(0xffffffffu, rs.f, src + 4);
     }
+    float amax = 0.f;
+#pragma unroll
+    for (int st = 1; st < D; st <<= 1)
+#pragma unroll
+        for (int g = 0; g < G; ++g)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                if (st < 8) {
+                    if (i & st) continue;
+                    const float u = x[g][i], v = x[g][i | (st & 7)];
+                    x[g][i] = u + v;
+                    x[g][i | (st & 7)] = u - v;
+                } else if (st < 32) {
+                    const float o = __shfl_xor_sync(0xffffffffu, x[g][i], st / 8);
+                    x[g][i] = (lane & (st / 8)) ? o - x[g][i] : x[g][i] + o;
+                } else {
+                    if (g & (st / 32)) continue;
+                    const float u = x[g][i], v = x[(g | (st / 32)) % G][i];
+                    x[g][i] = u + v;
+                    x[(g | (st / 32)) % G][i] = u - v;
+                }
+            }
+#pragma unroll
+    for (int g = 0; g < G; ++g)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(x[g][i]));
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+    const AttRowScale rs = att_row_scale<D>(a, amax);
+    const int src = (lane & 3) * 8;  // lane of row 2 j
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float u = x[g][i] * rs.up, v = x[g][i + 4] * rs.up;
+            const float dn = __uint_as_float((uint32_t)(127 - field_at(a.pg.kb, i)) << 23);
+            float ud = u * dn, vd = v * dn;
+            if (a.pg.kb == 4 && !(i & 1)) {
+                ud = fmaf(x[g][(i + 1) & 3] * rs.up, -0.0625f, ud);
+                vd = fmaf(x[g][4 + ((i + 1) & 3)] * rs.up, -0.0625f, vd);
+            }
+            const __half2 hi = __floats2half2_rn(ud, vd);
+            q.hi[g][i] = h2_bits(hi);
+            q.lo[g][i] = h2_bits(__floats2half2_rn(ud - __low2float(hi), vd - __high2float(hi)));
+            sum += u + v;
+        }
+        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+        sum *= rs.zero;
+        q.set_zero(g, __shfl_sync(0xffffffffu, sum, src), __shfl_sync(0xffffffffu, sum, src + 4));
+    }
+    q.f[0] = __shfl_sync(0xffffffffu, rs.f, src);
+    q.f[1] = __shfl_sync(0xffffffffu, rs.f, src + 4);
 }
 
-template <int D, int NT>
-QG_DEV void load_queries(const float* area, int lane, AttQ<D, NT>& q) {
-    using C = AttCfg<D, NT>;
+template <int D>
+QG_DEV void load_queries(const float* area, int lane, AttQ<D>& q) {
+    using C = AttCfg<D>;
     constexpr int G = D / 32;
     const uint4* f = reinterpret_cast<const uint4*>(area);
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-        for (int g = 0; g < G; ++g) {
-            const uint4 h = f[((nt * G + g) * 2) * 32 + lane], l = f[((nt * G + g) * 2 + 1) * 32 + lane];
-            q.hi[nt][g][0] = h.x, q.hi[nt][g][1] = h.y, q.hi[nt][g][2] = h.z, q.hi[nt][g][3] = h.w;
-            q.lo[nt][g][0] = l.x, q.lo[nt][g][1] = l.y, q.lo[nt][g][2] = l.z, q.lo[nt][g][3] = l.w;
-            const float2 z = *reinterpret_cast<const float2*>(area + C::QZero + (nt * G + g) * 8 + 2 * (lane & 3));
-            q.set_zero(nt, g, z.x, z.y);
-        }
-        const float2 v = *reinterpret_cast<const float2*>(area + C::QFactor + nt * 8 + 2 * (lane & 3));
-        q.f[nt][0] = v.x;
-        q.f[nt][1] = v.y;
+    for (int g = 0; g < G; ++g) {
+        const uint4 h = f[(g * 2) * 32 + lane], l = f[(g * 2 + 1) * 32 + lane];
+        q.hi[g][0] = h.x, q.hi[g][1] = h.y, q.hi[g][2] = h.z, q.hi[g][3] = h.w;
+        q.lo[g][0] = l.x, q.lo[g][1] = l.y, q.lo[g][2] = l.z, q.lo[g][3] = l.w;
+        const float2 z = *reinterpret_cast<const float2*>(area + C::QZero + g * 8 + 2 * (lane & 3));
+        q.set_zero(g, z.x, z.y);
     }
+    const float2 v = *reinterpret_cast<const float2*>(area + C::QFactor + 2 * (lane & 3));
+    q.f[0] = v.x;
+    q.f[1] = v.y;
 }
 
 // ------------------------------------------------------------------- output
@@ -571,13 +557,13 @@ QG_DEV void v_fields(const uint8_t* part, int half, int lane, uint32_t (&f)[D / 
     }
 }
 
-// acc += (codes of V) x (weights times scales): half a tile.  w[nt][c]: the weight of
-// token 16 half + 8 (c / 2) + r for row 8 nt + 2 j + c % 2.  The product with the
+// acc += (codes of V) x (weights times scales): half a tile.  w[c]: the weight of
+// token 16 half + 8 (c / 2) + r for row 2 j + c % 2.  The product with the
 // group's scale is taken in fp32 and rounded once, to the fp16 of the B operand;
 // movmatrix turns it from [token][row] to [row][token].
-template <int D, int NT, bool Masked>
+template <int D, bool Masked>
 QG_DEV void v_product(const uint8_t* scales, int half, int lane, const uint32_t (&f)[D / 32][2][4],
-                      const float (&w)[NT][4], float (&acc)[NT][D / 16][4]) {
+                      const float (&w)[4], float (&acc)[D / 16][4]) {
     constexpr int G = D / 32;
     const int r = lane >> 2;
     const uint32_t pick = (r & 1) ? 0x7632u : 0x5410u;  // u of token 8 tt + r
@@ -587,29 +573,26 @@ QG_DEV void v_product(const uint8_t* scales, int half, int lane, const uint32_t 
         const uint2 su = *reinterpret_cast<const uint2*>(scales + g * 16);
         const __half2 sh = bits_h2(__byte_perm(su.x, su.y, pick));
         const float s0 = __low2float(sh), s1 = __high2float(sh);
+        float b[4];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            float b[4];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                b[c] = w[nt][c] * (c < 2 ? s0 : s1);
-                if constexpr (Masked) b[c] = w[nt][c] == 0.f ? 0.f : b[c];  // whatever the scale it meets
-            }
-            const uint32_t b0 = movm_trans(h2_bits(__floats2half2_rn(b[0], b[1])));
-            const uint32_t b1 = movm_trans(h2_bits(__floats2half2_rn(b[2], b[3])));
-            mma_f16(acc[nt][2 * g], f[g][0][0], f[g][0][1], f[g][1][0], f[g][1][1], b0, b1);
-            mma_f16(acc[nt][2 * g + 1], f[g][0][2], f[g][0][3], f[g][1][2], f[g][1][3], b0, b1);
+        for (int c = 0; c < 4; ++c) {
+            b[c] = w[c] * (c < 2 ? s0 : s1);
+            if constexpr (Masked) b[c] = w[c] == 0.f ? 0.f : b[c];  // whatever the scale it meets
         }
+        const uint32_t b0 = movm_trans(h2_bits(__floats2half2_rn(b[0], b[1])));
+        const uint32_t b1 = movm_trans(h2_bits(__floats2half2_rn(b[2], b[3])));
+        mma_f16(acc[2 * g], f[g][0][0], f[g][0][1], f[g][1][0], f[g][1][1], b0, b1);
+        mma_f16(acc[2 * g + 1], f[g][0][2], f[g][0][3], f[g][1][2], f[g][1][3], b0, b1);
     }
 }
 
-template <int D, int NT, int B, bool Masked>
-QG_DEV void output_tile(const uint8_t* part, int lane, const float (&w)[2][NT][4], float (&acc)[NT][D / 16][4]) {
+template <int D, int B, bool Masked>
+QG_DEV void output_tile(const uint8_t* part, int lane, const float (&w)[2][4], float (&acc)[D / 16][4]) {
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
         uint32_t f[D / 32][2][4];
         v_fields<D, B>(part, half, lane, f);
-        v_product<D, NT, Masked>(part + 4 * D * B, half, lane, f, w[half], acc);
+        v_product<D, Masked>(part + 4 * D * B, half, lane, f, w[half], acc);
     }
 }
 
@@ -735,13 +718,13 @@ QG_DEV void store_row(const KvAttend& a, float (&o)[D / 32], float m, float l, i
 // KB, VB: the widths, or 0 where they are read from `a`.  Known widths make a tile's
 // work one run of instructions that hides the softmax's latency behind the codes' masks:
 // 131072 tokens at 4 bits 50 us against 56.5; they are built for 4/4 and 8/8.
-template <int D, int NT, int KB, int VB>
-__global__ void __launch_bounds__(AttCfg<D, NT>::T, 1) kv_attend_kernel(KvAttend a) {
+template <int D, int KB, int VB>
+__global__ void __launch_bounds__(AttCfg<D>::T, 1) kv_attend_kernel(KvAttend a) {
     if constexpr (KB > 0) {
         a.pg.kb = KB;
         a.pg.vb = VB;
     }
-    using C = AttCfg<D, NT>;
+    using C = AttCfg<D>;
     constexpr int W = C::W, G = C::G, RB = C::RB, E = D / 32, T = C::T;
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ long long sh_total[W];
@@ -894,12 +877,12 @@ __global__ void __launch_bounds__(AttCfg<D, NT>::T, 1) kv_attend_kernel(KvAttend
     if (shared_q)
         for (int i = 0; i < items; ++i)
             for (int r = (warp + W - i * RB % W) % W; r < RB; r += W)
-                rotate_query<D, NT>(a, raw + (i * RB + r) * D, areas + i * C::QFloats, r >> 3, r & 7, lane);
+                rotate_query<D>(a, raw + (i * RB + r) * D, areas + i * C::QFloats, r, lane);
     __syncthreads();
 
     // ---- one warp's run, item by item
-    AttQ<D, NT> q;
-    float acc[NT][2 * G][4], mo[NT][2], l[NT][2];  // weights are 2^(x - mo)
+    AttQ<D> q;
+    float acc[2 * G][4], mo[2], l[2];  // weights are 2^(x - mo)
     int stage = 0, parity = 0, rec_at = 0;
     const int j = lane & 3, r8 = lane >> 2;
     for (long long at = w0; count > 0;) {
@@ -907,67 +890,61 @@ __global__ void __launch_bounds__(AttCfg<D, NT>::T, 1) kv_attend_kernel(KvAttend
         const int n_tiles = min(count, cs.tiles - cc.tile);  // of this item, here
         const int rows = cs.n * a.group, r_base = cc.rb * RB;
         if (shared_q)
-            load_queries<D, NT>(areas + my_item * C::QFloats, lane, q);
+            load_queries<D>(areas + my_item * C::QFloats, lane, q);
         else
-            rotate_queries<D, NT>(a, cs.row0, rows, r_base, cc.h, lane, q);
+            rotate_queries<D>(a, cs.row0, rows, r_base, cc.h, lane, q);
         ++my_item;
         const bool fine = a.pg.kb <= 5 && cs.tiles <= kAttFine / kTileTokens;
-        if (fine)
+        if (fine) {
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
+            for (int g = 0; g < G; ++g)
 #pragma unroll
-                for (int g = 0; g < G; ++g)
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) q.zq[nt][g][c] *= 1024.f;
-                q.f[nt][0] *= 1.f / 1024.f;
-                q.f[nt][1] *= 1.f / 1024.f;
-            }
+                for (int c = 0; c < 4; ++c) q.zq[g][c] *= 1024.f;
+            q.f[0] *= 1.f / 1024.f;
+            q.f[1] *= 1.f / 1024.f;
+        }
         const int lo_pos = cs.pos0 + r_base / a.group;
         const int hi_pos = cs.pos0 + (min(r_base + RB, rows) - 1) / a.group;
         // tiles [u0, u1) of these are seen whole by every row
         const int t_base = (cs.t0 + cc.tile) * kTileTokens;
         const int u1 = (lo_pos + 1 - t_base) >> 5, u0 = a.window > 0 ? ((hi_pos - a.window - t_base) >> 5) + 1 : 0;
-        int qpos[NT][2], ve = kAttLowest;  // ve: exponent of the largest V scale seen
-        float limit[NT][2];       // a score may reach this before mo moves
+        int qpos[2], ve = kAttLowest;  // ve: exponent of the largest V scale seen
+        float limit[2];       // a score may reach this before mo moves
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int c = 0; c < 2; ++c) {
+            qpos[c] = cs.pos0 + (r_base + 2 * j + c) / a.group;
+            mo[c] = limit[c] = kAttNone;
+            l[c] = 0.f;
+        }
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                qpos[nt][c] = cs.pos0 + (r_base + 8 * nt + 2 * j + c) / a.group;
-                mo[nt][c] = limit[nt][c] = kAttNone;
-                l[nt][c] = 0.f;
-            }
+        for (int i = 0; i < 2 * G; ++i)
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int i = 0; i < 2 * G; ++i)
-#pragma unroll
-                for (int c = 0; c < 4; ++c) acc[nt][i][c] = 0.f;
+            for (int c = 0; c < 4; ++c) acc[i][c] = 0.f;
 #pragma unroll 1
         for (int it = 0; it < n_tiles; ++it) {
             if (!mbar_try_wait(&full[stage], parity) && !dead && !mbar_wait(&full[stage], parity)) dead = true;
             // (given up: no copy is issued any more and nothing is waited for; the run goes on over
             // whatever the ring holds, and the error word says so)
-            float s[2][NT][4];
+            float s[2][4];
             const uint8_t* rec = ring + rec_at;
             const uint8_t* vpart = rec + k_bytes;
             {
                 if constexpr (KB > 5) {
-                    scores_tile<D, NT, KB, false>(rec, lane, q, s);
+                    scores_tile<D, KB, false>(rec, lane, q, s);
                 } else if constexpr (KB > 0) {
                     if (fine)
-                        scores_tile<D, NT, KB, true>(rec, lane, q, s);
+                        scores_tile<D, KB, true>(rec, lane, q, s);
                     else
-                        scores_tile<D, NT, KB, false>(rec, lane, q, s);
+                        scores_tile<D, KB, false>(rec, lane, q, s);
                 } else {
                     switch (fine ? a.pg.kb + 8 : a.pg.kb) {
 #define QG_SCORES(B)                                   \
     case B:                                            \
-        scores_tile<D, NT, B, false>(rec, lane, q, s); \
+        scores_tile<D, B, false>(rec, lane, q, s); \
         break;
 #define QG_SCORES_FINE(B)                             \
     case B + 8:                                       \
-        scores_tile<D, NT, B, true>(rec, lane, q, s); \
+        scores_tile<D, B, true>(rec, lane, q, s); \
         break;
                         QG_SCORES(2)
                         QG_SCORES(3)
@@ -995,37 +972,30 @@ __global__ void __launch_bounds__(AttCfg<D, NT>::T, 1) kv_attend_kernel(KvAttend
 #pragma unroll
                     for (int h = 0; h < 2; ++h)
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                            for (int c = 0; c < 4; ++c) {
-                                const int t = t_first + 16 * h + 8 * (c >> 1) + r8, pos = qpos[nt][c & 1];
-                                if (t > pos || none || (a.window > 0 && t <= pos - a.window)) s[h][nt][c] = -INFINITY;
-                            }
+                        for (int c = 0; c < 4; ++c) {
+                            const int t = t_first + 16 * h + 8 * (c >> 1) + r8, pos = qpos[c & 1];
+                            if (t > pos || none || (a.window > 0 && t <= pos - a.window)) s[h][c] = -INFINITY;
+                        }
                 }
                 // Weights are 2^(x - mo): at most 2^(10 - ve) when mo is set, and it is moved when one
                 // would pass 2^(14 - ve), so that weight times scale (below 2^(ve + 1)) fits fp16.
                 // (The weights are computed before it is known, again if it has to be moved.)
-                float w[2][NT][4];
+                float w[2][4];
                 auto weigh = [&] {
 #pragma unroll
                     for (int h = 0; h < 2; ++h)
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                            for (int c = 0; c < 4; ++c)
-                                w[h][nt][c] = ex2(fmaf(s[h][nt][c], q.f[nt][c & 1], -mo[nt][c & 1]));
+                        for (int c = 0; c < 4; ++c)
+                            w[h][c] = ex2(fmaf(s[h][c], q.f[c & 1], -mo[c & 1]));
                 };
                 weigh();
-                float tm[NT][2];
+                float tm[2];
                 bool over = false;
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        tm[nt][c] = q.f[nt][c] *
-                                    fmaxf(fmaxf(s[0][nt][c], s[0][nt][c + 2]), fmaxf(s[1][nt][c], s[1][nt][c + 2]));
-                        over |= tm[nt][c] > limit[nt][c];
-                    }
+                for (int c = 0; c < 2; ++c) {
+                    tm[c] = q.f[c] * fmaxf(fmaxf(s[0][c], s[0][c + 2]), fmaxf(s[1][c], s[1][c + 2]));
+                    over |= tm[c] > limit[c];
+                }
                 const __half2 vmax = v_scale_max<D>(vpart, a.pg.vb, lane, last);
                 over |= !__hblt2(vmax, bits_h2((uint32_t)(16 + ve) * 0x04000400u));  // 2^(ve + 1), infinity for 15
                 if (__any_sync(0xffffffffu, over)) {
@@ -1034,46 +1004,42 @@ __global__ void __launch_bounds__(AttCfg<D, NT>::T, 1) kv_attend_kernel(KvAttend
                     for (int o = 1; o < 32; o <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, o));
                     const int vn = min(max((int)(__float_as_uint(t) >> 23) - 127, ve), 15);
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
+                    for (int c = 0; c < 2; ++c) {
+                        t = tm[c];
 #pragma unroll
-                        for (int c = 0; c < 2; ++c) {
-                            t = tm[nt][c];
+                        for (int o = 4; o < 32; o <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, o));
+                        const float mn = fmaxf(mo[c] + (float)(vn - ve), t - (float)(10 - vn));
+                        const float k = mo[c] == mn ? 1.f : ex2(mo[c] - mn);
+                        mo[c] = mn;
+                        limit[c] = mn + (float)(14 - vn);
+                        l[c] *= k;
 #pragma unroll
-                            for (int o = 4; o < 32; o <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, o));
-                            const float mn = fmaxf(mo[nt][c] + (float)(vn - ve), t - (float)(10 - vn));
-                            const float k = mo[nt][c] == mn ? 1.f : ex2(mo[nt][c] - mn);
-                            mo[nt][c] = mn;
-                            limit[nt][c] = mn + (float)(14 - vn);
-                            l[nt][c] *= k;
-#pragma unroll
-                            for (int i = 0; i < 2 * G; ++i) {
-                                acc[nt][i][c] *= k;
-                                acc[nt][i][c + 2] *= k;
-                            }
+                        for (int i = 0; i < 2 * G; ++i) {
+                            acc[i][c] *= k;
+                            acc[i][c + 2] *= k;
                         }
+                    }
                     ve = vn;
                     weigh();
                 }
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        l[nt][0] += w[h][nt][0] + w[h][nt][2];
-                        l[nt][1] += w[h][nt][1] + w[h][nt][3];
-                    }
+                for (int h = 0; h < 2; ++h) {
+                    l[0] += w[h][0] + w[h][2];
+                    l[1] += w[h][1] + w[h][3];
+                }
                 if constexpr (VB > 0) {
                     if (masked)
-                        output_tile<D, NT, VB, true>(vpart, lane, w, acc);
+                        output_tile<D, VB, true>(vpart, lane, w, acc);
                     else
-                        output_tile<D, NT, VB, false>(vpart, lane, w, acc);
+                        output_tile<D, VB, false>(vpart, lane, w, acc);
                 } else {
                     switch (a.pg.vb) {
 #define QG_OUTPUT(B)                                               \
     case B:                                                        \
         if (masked)                                                \
-            output_tile<D, NT, B, true>(vpart, lane, w, acc);      \
+            output_tile<D, B, true>(vpart, lane, w, acc);      \
         else                                                       \
-            output_tile<D, NT, B, false>(vpart, lane, w, acc);     \
+            output_tile<D, B, false>(vpart, lane, w, acc);     \
         break;
                         QG_OUTPUT(2)
                         QG_OUTPUT(3)
@@ -1100,100 +1066,92 @@ __global__ void __launch_bounds__(AttCfg<D, NT>::T, 1) kv_attend_kernel(KvAttend
         float* slot = frag_head ? reinterpret_cast<float*>(ring) : slots + warp * C::SlotFloats;
         AttFrag& fr = frags[warp * 2 + (frag_head ? 1 : 0)];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int i = 0; i < 2 * G; ++i)
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    float &u = acc[nt][i][c], &v = acc[nt][i][c + 2];  // fields 2 (i % 2) and the next
-                    u *= __uint_as_float((uint32_t)(127 + 14 - field_at(a.pg.vb, 2 * (i & 1))) << 23);
-                    v *= __uint_as_float((uint32_t)(127 + 14 - field_at(a.pg.vb, 2 * (i & 1) + 1)) << 23);
-                    if (a.pg.vb == 4) v -= u * 0.0625f;
-                }
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int i = 0; i < 2 * G; ++i)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-#pragma unroll
-                for (int o = 4; o < 32; o <<= 1) l[nt][c] += __shfl_xor_sync(0xffffffffu, l[nt][c], o);
+                float &u = acc[i][c], &v = acc[i][c + 2];  // fields 2 (i % 2) and the next
+                u *= __uint_as_float((uint32_t)(127 + 14 - field_at(a.pg.vb, 2 * (i & 1))) << 23);
+                v *= __uint_as_float((uint32_t)(127 + 14 - field_at(a.pg.vb, 2 * (i & 1) + 1)) << 23);
+                if (a.pg.vb == 4) v -= u * 0.0625f;
             }
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) l[c] += __shfl_xor_sync(0xffffffffu, l[c], o);
+        }
         if (frag_head && cc.tile + n_tiles == cs.tiles) {
             // the whole item: rotate back in this layout (dim 32 g + 4 r + i) and store
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int c = 0; c < 2; ++c) {
+                float x[G][4];
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    float x[G][4];
+                for (int g = 0; g < G; ++g)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) x[g][i] = acc[2 * g + (i >> 1)][(i & 1) * 2 + c];
+#pragma unroll
+                for (int g = 0; g < G; ++g) {
+#pragma unroll
+                    for (int st = 1; st < 4; st <<= 1)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (!(i & st)) {
+                                const float u = x[g][i], v = x[g][i + st];
+                                x[g][i] = u + v;
+                                x[g][i + st] = u - v;
+                            }
+#pragma unroll
+                    for (int ls = 4; ls < 32; ls <<= 1)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float o = __shfl_xor_sync(0xffffffffu, x[g][i], ls);
+                            x[g][i] = (lane & ls) ? o - x[g][i] : x[g][i] + o;
+                        }
+                }
+#pragma unroll
+                for (int st = 1; st < G; st <<= 1)
 #pragma unroll
                     for (int g = 0; g < G; ++g)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) x[g][i] = acc[nt][2 * g + (i >> 1)][(i & 1) * 2 + c];
-#pragma unroll
-                    for (int g = 0; g < G; ++g) {
-#pragma unroll
-                        for (int st = 1; st < 4; st <<= 1)
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                if (!(i & st)) {
-                                    const float u = x[g][i], v = x[g][i + st];
-                                    x[g][i] = u + v;
-                                    x[g][i + st] = u - v;
-                                }
-#pragma unroll
-                        for (int ls = 4; ls < 32; ls <<= 1)
+                        if (!(g & st))
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
-                                const float o = __shfl_xor_sync(0xffffffffu, x[g][i], ls);
-                                x[g][i] = (lane & ls) ? o - x[g][i] : x[g][i] + o;
+                                const float u = x[g][i], v = x[g + st][i];
+                                x[g][i] = u + v;
+                                x[g + st][i] = u - v;
                             }
+                const int r = r_base + 2 * j + c;
+                if (r < rows) {
+                    const int tok = r / a.group, hq = cc.h * a.group + (r - tok * a.group);
+                    const float inv = l[c] == 0.f ? 0.f : 1.f / (l[c] * (float)D);
+                    uint16_t* o = reinterpret_cast<uint16_t*>(a.out.p) + (cs.row0 + tok) * a.out.row +
+                                  hq * a.out.head + 4 * r8;
+#pragma unroll
+                    for (int g = 0; g < G; ++g) {
+                        uint16_t v[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) v[i] = att_out(a, x[g][i] * inv);
+                        *reinterpret_cast<uint2*>(o + 32 * g) =
+                            make_uint2(v[0] | (uint32_t)v[1] << 16, v[2] | (uint32_t)v[3] << 16);
                     }
-#pragma unroll
-                    for (int st = 1; st < G; st <<= 1)
-#pragma unroll
-                        for (int g = 0; g < G; ++g)
-                            if (!(g & st))
-#pragma unroll
-                                for (int i = 0; i < 4; ++i) {
-                                    const float u = x[g][i], v = x[g + st][i];
-                                    x[g][i] = u + v;
-                                    x[g + st][i] = u - v;
-                                }
-                    const int r = r_base + 8 * nt + 2 * j + c;
-                    if (r < rows) {
-                        const int tok = r / a.group, hq = cc.h * a.group + (r - tok * a.group);
-                        const float inv = l[nt][c] == 0.f ? 0.f : 1.f / (l[nt][c] * (float)D);
-                        uint16_t* o = reinterpret_cast<uint16_t*>(a.out.p) + (cs.row0 + tok) * a.out.row +
-                                      hq * a.out.head + 4 * r8;
-#pragma unroll
-                        for (int g = 0; g < G; ++g) {
-                            uint16_t v[4];
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) v[i] = att_out(a, x[g][i] * inv);
-                            *reinterpret_cast<uint2*>(o + 32 * g) =
-                                make_uint2(v[0] | (uint32_t)v[1] << 16, v[2] | (uint32_t)v[3] << 16);
-                        }
-                        if (a.lse && r8 == 0)
-                            a.lse[(int64_t)(cs.row0 + tok) * a.q_heads + hq] =
-                                (mo[nt][c] + log2f(l[nt][c])) * 0.6931471805599453f;
-                    }
+                    if (a.lse && r8 == 0)
+                        a.lse[(int64_t)(cs.row0 + tok) * a.q_heads + hq] =
+                            (mo[c] + log2f(l[c])) * 0.6931471805599453f;
                 }
+            }
         } else {
             __syncwarp();
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int c = 0; c < 2; ++c) {
+                const int r = 2 * j + c;
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    const int r = 8 * nt + 2 * j + c;
-#pragma unroll
-                    for (int g = 0; g < G; ++g)
-                        *reinterpret_cast<float4*>(slot + r * C::OS + 32 * g + 4 * r8) =
-                            make_float4(acc[nt][2 * g][c], acc[nt][2 * g][c + 2], acc[nt][2 * g + 1][c],
-                                        acc[nt][2 * g + 1][c + 2]);
-                    if (r8 == 0) {
-                        slot[RB * C::OS + r] = mo[nt][c];
-                        slot[RB * C::OS + RB + r] = l[nt][c];
-                    }
+                for (int g = 0; g < G; ++g)
+                    *reinterpret_cast<float4*>(slot + r * C::OS + 32 * g + 4 * r8) =
+                        make_float4(acc[2 * g][c], acc[2 * g][c + 2], acc[2 * g + 1][c],
+                                    acc[2 * g + 1][c + 2]);
+                if (r8 == 0) {
+                    slot[RB * C::OS + r] = mo[c];
+                    slot[RB * C::OS + RB + r] = l[c];
                 }
+            }
             if (lane == 0) {
                 // the item's first tile as a number of the call
                 fr.item = at - cc.tile;

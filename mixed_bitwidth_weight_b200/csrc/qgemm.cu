@@ -33,7 +33,7 @@ struct DeviceInfo {
     bool int_attr[3] = {false, false, false};
     bool gemm_attr[2] = {false, false};
     bool quant_attr = false;
-    bool attend_attr[3][2][3] = {};  // [head size][row tiles][widths]
+    bool attend_attr[3][3] = {};  // [head size][widths]
 };
 
 DeviceInfo g_devs[64];
@@ -944,24 +944,15 @@ int kv_move(bool append, const qgemm_kv_cache* cache, const qgemm_kv_batch* batc
     return launch_status();
 }
 
-// Row tiles of the attention kernel: two (16 query rows an item) when a
-// sequence brings more than 8 rows on average, except for 256 dims, whose
-// accumulators for 16 rows would not fit the registers.
-int attend_row_tiles(int D, int64_t rows, int num_seqs, int group) {
-    if (D == 256) return 1;
-    return (rows + num_seqs - 1) / num_seqs * group > 8 ? 2 : 1;
-}
-
 constexpr size_t kAttendTicketBytes = 1024;  // one counter per CTA
 
 size_t attend_ws_bytes(int D, int sms) {
-    const size_t rows = D == 256 ? 8 : 16;
-    return kAttendTicketBytes + (size_t)sms * 2 * rows * (D + 2) * 4;
+    return kAttendTicketBytes + (size_t)sms * 2 * 8 * (D + 2) * 4;  // two fragments of 8 rows a CTA
 }
 
-template <int D, int NT, int KB, int VB>
+template <int D, int KB, int VB>
 int launch_attend(KvAttend a, DeviceInfo* dev, bool* attr, cudaStream_t s) {
-    using C = AttCfg<D, NT>;
+    using C = AttCfg<D>;
     constexpr size_t most = 226 * 1024;  // 227 KB a CTA, some of it static
     // the ring's stages are whole records; at the end it also takes a fragment
     const size_t rec = (size_t)4 * D * (a.pg.kb + a.pg.vb + 1), room = (most - C::RingAt) / C::W / 128 * 128;
@@ -969,7 +960,7 @@ int launch_attend(KvAttend a, DeviceInfo* dev, bool* attr, cudaStream_t s) {
     a.ring_bytes = (int)((std::max(a.stages * rec, (size_t)C::SlotBytes) + 127) / 128 * 128);
     if (a.stages < 1 || (size_t)a.ring_bytes > room) return QGEMM_ERR_UNSUPPORTED;
     if (!*attr) {  // a per-device setting
-        if (cudaFuncSetAttribute(kv_attend_kernel<D, NT, KB, VB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        if (cudaFuncSetAttribute(kv_attend_kernel<D, KB, VB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  (int)most) != cudaSuccess) {
             cudaGetLastError();
             return QGEMM_ERR_CUDA;
@@ -977,7 +968,7 @@ int launch_attend(KvAttend a, DeviceInfo* dev, bool* attr, cudaStream_t s) {
         *attr = true;
     }
     static_assert(C::MaxCtas * 4 <= kAttendTicketBytes, "a ticket for each CTA");
-    kv_attend_kernel<D, NT, KB, VB><<<std::min(dev->sms, C::MaxCtas), C::T, C::RingAt + C::W * a.ring_bytes, s>>>(a);
+    kv_attend_kernel<D, KB, VB><<<std::min(dev->sms, C::MaxCtas), C::T, C::RingAt + C::W * a.ring_bytes, s>>>(a);
     return launch_status();
 }
 
@@ -1381,20 +1372,17 @@ int qgemm_kv_attend(const qgemm_kv_cache* cache, const qgemm_kv_batch* batch, in
     a.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(d_ws) + kAttendTicketBytes);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     a.bf16 = dtype == QGEMM_BF16;
-    const int nt = attend_row_tiles(D, a.bt.rows, a.bt.num_seqs, a.group);
     const int known = a.pg.kb != a.pg.vb ? 0 : a.pg.kb == 4 ? 1 : a.pg.kb == 8 ? 2 : 0;
-#define QG_ATTEND(DD, NT, I)                                                                 \
-    if (D == DD && nt == NT) {                                                               \
-        bool* attr = &dev->attend_attr[I][NT - 1][known];                                    \
-        return known == 1   ? launch_attend<DD, NT, 4, 4>(a, dev, attr, s)                   \
-               : known == 2 ? launch_attend<DD, NT, 8, 8>(a, dev, attr, s)                   \
-                            : launch_attend<DD, NT, 0, 0>(a, dev, attr, s);                  \
+#define QG_ATTEND(DD, I)                                                                 \
+    if (D == DD) {                                                                       \
+        bool* attr = &dev->attend_attr[I][known];                                        \
+        return known == 1   ? launch_attend<DD, 4, 4>(a, dev, attr, s)                   \
+               : known == 2 ? launch_attend<DD, 8, 8>(a, dev, attr, s)                   \
+                            : launch_attend<DD, 0, 0>(a, dev, attr, s);                  \
     }
-    QG_ATTEND(64, 1, 0)
-    QG_ATTEND(64, 2, 0)
-    QG_ATTEND(128, 1, 1)
-    QG_ATTEND(128, 2, 1)
-    QG_ATTEND(256, 1, 2)
+    QG_ATTEND(64, 0)
+    QG_ATTEND(128, 1)
+    QG_ATTEND(256, 2)
 #undef QG_ATTEND
     return QGEMM_ERR_UNSUPPORTED;
 }
