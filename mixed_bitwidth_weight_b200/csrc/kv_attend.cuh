@@ -9,31 +9,41 @@
 //
 // Scores, per group g of 32 dims: sum_d (Hq)_d (c - z) on m16n8k16 with the
 // codes as the A operand (16 tokens), 8 query rows as B.  A code's bits, masked
-// out of its word, ARE an fp16 number: the subnormal c 2^-24 (in place, i bits
-// further up, c 2^(i-24); the query carries 2^-i).  So a pair of codes costs one
-// AND.  The accumulators start at -z sum_d (Hq)_d instead of 0, and the token's
-// scale multiplies the group's sum in fp32.  The rotated query is held as two
-// fp16 parts (22 bits), each times the exact codes.
-// Output: A = codes of V (16 dims x 16 tokens; c - z by one exact subtraction
-// per pair: starting at -z sum p would lose the sum of many tokens to
-// cancellation), B = p s_g, rounded to fp16 after p and s are (two roundings of
-// 2^-12 on average per weight; the sum of weights is not rounded).  p is kept
-// near 2^10 and s below 2 (2^-E of the largest seen) so that weights keep 11
-// bits down to 2^-24 of the largest.  P turns from the accumulators' layout to
-// the B operand's by movmatrix.
+// out of its word, ARE an fp16 number: the subnormal c 2^-24 (or, i bits further
+// up where it lies, c 2^(i-24); the query carries 2^-i).  So a pair of codes costs
+// one AND.  The accumulators start at -z sum_d (Hq)_d instead of 0, and the
+// token's scale multiplies the group's sum in fp32.  The rotated query is held as
+// two fp16 parts (22 bits, scaled by the row's power of two), each times the exact
+// codes.
+// Output: A = codes of V (16 dims x 16 tokens), c - z by one exact fused
+// multiply-add a pair (starting at -z sum p would lose the sum of many tokens to
+// cancellation), B = p s_g.  p, s and their product are fp32, the product is
+// rounded once to fp16 (2^-12 on average; rounding p first cost a third more error
+// and saved 4% of the time), the sum of weights is not rounded.  p is scaled so that the
+// products stay below 2^15 and weights keep 11 bits down to 2^-24 of the largest.
+// The products turn from [token][row] to the B operand's [row][token] by movmatrix.
 //
 // The legacy matrix instruction, because its operands are registers: a code is
 // masked into place and multiplied without a store.  tcgen05 would need every
 // expanded tile written to tensor or shared memory first (the V tile transposed),
-// and 8 query rows fill 1/16 of its M.  m16n8k16 runs at 2.1 cycles per SM here;
-// 24 of them per 16 tokens of 128 dims are 50 cycles against the 100 the codes
-// (144 bytes a token at 4 bits) take from HBM.
+// and 8 query rows fill 1/16 of its M.
 //
-// Work: the (sequence, head, block of rows, 32-token tile) space is cut into equal
-// runs per CTA and per warp, whatever the lengths (both read on the device).  A
-// warp walks its run with a ring of bulk copies (one record each); what it has of
-// an item is joined in shared memory per CTA, and across CTAs by the last one
-// to arrive, in a fixed order.
+// What bounds it: instructions, not HBM, below 8 bits.  A tile of 32 tokens of 128
+// dims at 4 bits takes about 540 instructions of a warp.  Measured on the four
+// schedulers, m16n8k16 takes 8.4 cycles, integer and fp16 instructions 2 each, and
+// they overlap little (one with four ANDs and four fp16 adds: 17.7 cycles of 24.4):
+// 300 cycles a tile and SM against the 200 that its 4608 bytes take from HBM.
+// 524288 tokens x 8 heads x 128: 4/4 bits 165 us (3.6 TB/s, 55% of measured HBM), 6/4
+// bits (393216 tokens) 162 us (3.4 TB/s), 8/8 bits (262144) 96-105 us (5.4-5.9 TB/s).
+//
+// Work: the (sequence, head, 8 rows, 32-token tile) space is cut into equal runs per
+// CTA and per warp, whatever the lengths (all read on the device).  A warp walks its
+// run with a ring of bulk copies (one record each; a separate feeding warp was slower,
+// per-lane asynchronous copies too); what it has of an item is joined in shared memory
+// per CTA, and across CTAs by the last one to arrive, in a fixed order, so results
+// repeat bit for bit.  Eight warps of up to 255 registers: twelve of 168 gained 4% on
+// long sequences and lost 15% on short ones, except at 64 dims.  Scan, seek, first copies
+// and join are about 8 us whatever the length.
 #pragma once
 
 #include "kv_paged.cuh"
@@ -716,8 +726,8 @@ QG_DEV void store_row(const KvAttend& a, float (&o)[D / 32], float m, float l, i
 }
 
 // KB, VB: the widths, or 0 where they are read from `a`.  Known widths make a tile's
-// work one run of instructions that hides the softmax's latency behind the codes' masks:
-// 131072 tokens at 4 bits 50 us against 56.5; they are built for 4/4 and 8/8.
+// work one run of instructions that hides the softmax's latency behind the codes' masks
+// (131072 tokens at 4 bits: 8% faster); they are built for 4/4 and 8/8.
 template <int D, int KB, int VB>
 __global__ void __launch_bounds__(AttCfg<D>::T, 1) kv_attend_kernel(KvAttend a) {
     if constexpr (KB > 0) {
