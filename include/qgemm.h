@@ -289,7 +289,8 @@ int qgemm_kv_append(const qgemm_kv_cache* cache, const qgemm_kv_batch* batch, in
                     void* stream);
 
 /* Reads the last n_b tokens of every sequence back (n_b = seq_len: all of it):
- * v' = H_D ((q - 2^(b-1)) s) / D, rounded once to dtype, into d_k and d_v. */
+ * v' = H_D ((q - 2^(b-1)) s) / D, rounded once to dtype, into d_k and d_v (which
+ * must not overlap each other). */
 int qgemm_kv_gather(const qgemm_kv_cache* cache, const qgemm_kv_batch* batch, int num_rows, void* d_k, int64_t k_row_stride,
                     int64_t k_head_stride, void* d_v, int64_t v_row_stride, int64_t v_head_stride, int dtype,
                     void* stream);

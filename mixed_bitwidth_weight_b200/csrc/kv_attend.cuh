@@ -63,12 +63,6 @@ struct KvAttend {
 };
 
 constexpr int kAttMaxStages = 8;
-// The matrix instruction aligns products by their operands' exponents, and a subnormal's is
-// that of 2^-14 whatever its leading zeros: codes of b bits lose up to 10 - b of the sum's 24
-// bits, which leaves a score 5e-6 of its size off at 2 to 4 bits.  The error averages out
-// over the tokens (the lse is 1e-6 off at 300, 4e-7 at 5000).  Rows that see up to kAttFine
-// tokens take their codes as normal numbers, one multiplication (exact) per pair: 3e-7.
-constexpr int kAttFine = 2048;
 constexpr int kAttLowest = -14;       // V scales below 2^-13 count as if they were that
 constexpr float kAttNone = -3.4e38f;  // the weights' offset before any token: below every finite score
 
@@ -302,10 +296,18 @@ QG_DEV void k_fragment(const uint32_t (&w)[D * B / 64], int g, int step, uint32_
 // Scores of a tile, s[half][c].  The four dependent matrix instructions of a
 // group are issued a step at a time over all groups, so that eight chains (four
 // with 64 dims) hide each other's latency.
-// Fine: the codes made normal numbers, times 2^10 (see kAttFine).
-template <int D, int B, bool Fine>
+// The matrix instruction aligns products by their operands' exponents, and a subnormal's
+// is that of 2^-14 whatever its leading zeros: codes of b bits would lose up to 10 - b of
+// the sum's 24 bits, 5e-6 of a score's size at 2 to 4 bits.  Up to 5 bits they are
+// therefore made normal numbers, times 2^10, by one exact multiplication a pair (3e-7,
+// and 2% of the time); the query's
+// factors know (att_row_scale).
+template <int B>
+constexpr bool kNorm = B <= 5;
+
+template <int D, int B>
 QG_DEV void scores_tile(const uint8_t* rec, int lane, const AttQ<D>& q, float (&s)[2][4]) {
-    constexpr int G = D / 32, NW = D * B / 64, HB = D > 128 ? 1 : 2;  // halves at a time
+    constexpr int G = D / 32, NW = D * B / 64, HB = D == 256 || (D == 128 && B <= 4) ? 1 : 2;  // halves at a time, as measured
 #pragma unroll
     for (int h0 = 0; h0 < 2; h0 += HB) {
         uint32_t w[HB][NW], sc[HB][G];
@@ -339,7 +341,7 @@ QG_DEV void scores_tile(const uint8_t* rec, int lane, const AttQ<D>& q, float (&
                 for (int g = 0; g < G; ++g) {
                     uint32_t(&x)[4] = a[h][g];
                     k_fragment<D, B>(w[h], g, step, x);
-                    if constexpr (Fine)
+                    if constexpr (kNorm<B>)
 #pragma unroll
                         for (int i = 0; i < 4; ++i) x[i] = h2_bits(__hmul2(bits_h2(x[i]), bits_h2(0x64006400u)));
                     if (step == 0)
@@ -388,8 +390,9 @@ QG_DEV AttRowScale att_row_scale(const KvAttend& a, float amax) {
     AttRowScale r;
     r.up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
     if (a.scale < 0.f) r.up = -r.up;
-    r.zero = -(float)(1 << (a.pg.kb - 1)) * 5.9604644775390625e-8f;
-    r.f = fmaxf(fabsf(a.scale) * (1.4426950408889634f / (float)D) * 16777216.f *
+    const float unit = a.pg.kb <= 5 ? 6.103515625e-5f : 5.9604644775390625e-8f;  // 2^-14 or 2^-24, see kNorm
+    r.zero = -(float)(1 << (a.pg.kb - 1)) * unit;
+    r.f = fmaxf(fabsf(a.scale) * (1.4426950408889634f / (float)D) / unit *
                     __uint_as_float((uint32_t)(127 - 14 + e) << 23),
                 1e-30f);
     return r;
@@ -533,7 +536,7 @@ QG_DEV void load_queries(const float* area, int lane, AttQ<D>& q) {
 
 // ------------------------------------------------------------------- output
 // A registers of half a tile's V codes, (c - z) 2^-14 in units of their fields, one exact
-// fused multiply-add a pair (which also makes them normal numbers, see kAttFine): f[g][k][i]
+// fused multiply-add a pair (which also makes them normal numbers, see kNorm): f[g][k][i]
 // holds field i of group g's dims for tokens 16 half + 8 k + 2 j + {0, 1}.
 template <int D, int B>
 QG_DEV void v_fields(const uint8_t* part, int half, int lane, uint32_t (&f)[D / 32][2][4]) {
@@ -904,15 +907,6 @@ __global__ void __launch_bounds__(AttCfg<D>::T, 1) kv_attend_kernel(KvAttend a) 
         else
             rotate_queries<D>(a, cs.row0, rows, r_base, cc.h, lane, q);
         ++my_item;
-        const bool fine = a.pg.kb <= 5 && cs.tiles <= kAttFine / kTileTokens;
-        if (fine) {
-#pragma unroll
-            for (int g = 0; g < G; ++g)
-#pragma unroll
-                for (int c = 0; c < 4; ++c) q.zq[g][c] *= 1024.f;
-            q.f[0] *= 1.f / 1024.f;
-            q.f[1] *= 1.f / 1024.f;
-        }
         const int lo_pos = cs.pos0 + r_base / a.group;
         const int hi_pos = cs.pos0 + (min(r_base + RB, rows) - 1) / a.group;
         // tiles [u0, u1) of these are seen whole by every row
@@ -938,112 +932,95 @@ __global__ void __launch_bounds__(AttCfg<D>::T, 1) kv_attend_kernel(KvAttend a) 
             float s[2][4];
             const uint8_t* rec = ring + rec_at;
             const uint8_t* vpart = rec + k_bytes;
-            {
-                if constexpr (KB > 5) {
-                    scores_tile<D, KB, false>(rec, lane, q, s);
-                } else if constexpr (KB > 0) {
-                    if (fine)
-                        scores_tile<D, KB, true>(rec, lane, q, s);
-                    else
-                        scores_tile<D, KB, false>(rec, lane, q, s);
-                } else {
-                    switch (fine ? a.pg.kb + 8 : a.pg.kb) {
-#define QG_SCORES(B)                                   \
-    case B:                                            \
-        scores_tile<D, B, false>(rec, lane, q, s); \
+            if constexpr (KB > 0) {
+                scores_tile<D, KB>(rec, lane, q, s);
+            } else {
+                switch (a.pg.kb) {
+#define QG_SCORES(B)                        \
+    case B:                                 \
+        scores_tile<D, B>(rec, lane, q, s); \
         break;
-#define QG_SCORES_FINE(B)                             \
-    case B + 8:                                       \
-        scores_tile<D, B, true>(rec, lane, q, s); \
-        break;
-                        QG_SCORES(2)
-                        QG_SCORES(3)
-                        QG_SCORES(4)
-                        QG_SCORES(5)
-                        QG_SCORES(6)
-                        QG_SCORES(8)
-                        QG_SCORES_FINE(2)
-                        QG_SCORES_FINE(3)
-                        QG_SCORES_FINE(4)
-                        QG_SCORES_FINE(5)
+                    QG_SCORES(2)
+                    QG_SCORES(3)
+                    QG_SCORES(4)
+                    QG_SCORES(5)
+                    QG_SCORES(6)
+                    QG_SCORES(8)
 #undef QG_SCORES
-#undef QG_SCORES_FINE
-                    }
                 }
             }
-            {
-                // a tile without a page shows nothing
-                const bool none = bad >> stage & 1;
-                const bool masked = it < u0 || it >= u1 || none;
-                int last = kTileTokens;  // last slot that any row sees
-                if (masked) {
-                    const int t_first = t_base + it * kTileTokens;
-                    last = none ? -1 : hi_pos - t_first;
+            // a tile without a page shows nothing
+            const bool none = bad >> stage & 1;
+            const bool masked = it < u0 || it >= u1 || none;
+            int last = kTileTokens;  // last slot that any row sees
+            if (masked) {
+                const int t_first = t_base + it * kTileTokens;
+                last = none ? -1 : hi_pos - t_first;
 #pragma unroll
-                    for (int h = 0; h < 2; ++h)
+                for (int h = 0; h < 2; ++h)
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            const int t = t_first + 16 * h + 8 * (c >> 1) + r8, pos = qpos[c & 1];
-                            if (t > pos || none || (a.window > 0 && t <= pos - a.window)) s[h][c] = -INFINITY;
-                        }
-                }
-                // Weights are 2^(x - mo): at most 2^(10 - ve) when mo is set, and it is moved when one
-                // would pass 2^(14 - ve), so that weight times scale (below 2^(ve + 1)) fits fp16.
-                // (The weights are computed before it is known, again if it has to be moved.)
-                float w[2][4];
-                auto weigh = [&] {
+                    for (int c = 0; c < 4; ++c) {
+                        const int t = t_first + 16 * h + 8 * (c >> 1) + r8, pos = qpos[c & 1];
+                        if (t > pos || none || (a.window > 0 && t <= pos - a.window)) s[h][c] = -INFINITY;
+                    }
+            }
+            // Weights are 2^(x - mo): at most 2^(10 - ve) when mo is set, and it is moved when one
+            // would pass 2^(14 - ve), so that weight times scale (below 2^(ve + 1)) fits fp16.
+            // (The weights are computed before it is known, again if it has to be moved.)
+            float w[2][4];
+            auto weigh = [&] {
 #pragma unroll
-                    for (int h = 0; h < 2; ++h)
+                for (int h = 0; h < 2; ++h)
 #pragma unroll
-                        for (int c = 0; c < 4; ++c)
-                            w[h][c] = ex2(fmaf(s[h][c], q.f[c & 1], -mo[c & 1]));
-                };
-                weigh();
-                float tm[2];
-                bool over = false;
+                    for (int c = 0; c < 4; ++c)
+                        w[h][c] = ex2(fmaf(s[h][c], q.f[c & 1], -mo[c & 1]));
+            };
+            weigh();
+            float tm[2];
+            bool over = false;
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                tm[c] = q.f[c] * fmaxf(fmaxf(s[0][c], s[0][c + 2]), fmaxf(s[1][c], s[1][c + 2]));
+                over |= tm[c] > limit[c];
+            }
+            const __half2 vmax = v_scale_max<D>(vpart, a.pg.vb, lane, last);
+            over |= !__hblt2(vmax, bits_h2((uint32_t)(16 + ve) * 0x04000400u));  // 2^(ve + 1), infinity for 15
+            if (__any_sync(0xffffffffu, over)) {
+                float t = fmaxf(__low2float(vmax), __high2float(vmax));
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, o));
+                const int vn = min(max((int)(__float_as_uint(t) >> 23) - 127, ve), 15);
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    tm[c] = q.f[c] * fmaxf(fmaxf(s[0][c], s[0][c + 2]), fmaxf(s[1][c], s[1][c + 2]));
-                    over |= tm[c] > limit[c];
-                }
-                const __half2 vmax = v_scale_max<D>(vpart, a.pg.vb, lane, last);
-                over |= !__hblt2(vmax, bits_h2((uint32_t)(16 + ve) * 0x04000400u));  // 2^(ve + 1), infinity for 15
-                if (__any_sync(0xffffffffu, over)) {
-                    float t = fmaxf(__low2float(vmax), __high2float(vmax));
+                    t = tm[c];
 #pragma unroll
-                    for (int o = 1; o < 32; o <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, o));
-                    const int vn = min(max((int)(__float_as_uint(t) >> 23) - 127, ve), 15);
+                    for (int o = 4; o < 32; o <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, o));
+                    const float mn = fmaxf(mo[c] + (float)(vn - ve), t - (float)(10 - vn));
+                    const float k = mo[c] == mn ? 1.f : ex2(mo[c] - mn);
+                    mo[c] = mn;
+                    limit[c] = mn + (float)(14 - vn);
+                    l[c] *= k;
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        t = tm[c];
-#pragma unroll
-                        for (int o = 4; o < 32; o <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, o));
-                        const float mn = fmaxf(mo[c] + (float)(vn - ve), t - (float)(10 - vn));
-                        const float k = mo[c] == mn ? 1.f : ex2(mo[c] - mn);
-                        mo[c] = mn;
-                        limit[c] = mn + (float)(14 - vn);
-                        l[c] *= k;
-#pragma unroll
-                        for (int i = 0; i < 2 * G; ++i) {
-                            acc[i][c] *= k;
-                            acc[i][c + 2] *= k;
-                        }
+                    for (int i = 0; i < 2 * G; ++i) {
+                        acc[i][c] *= k;
+                        acc[i][c + 2] *= k;
                     }
-                    ve = vn;
-                    weigh();
                 }
+                ve = vn;
+                weigh();
+            }
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    l[0] += w[h][0] + w[h][2];
-                    l[1] += w[h][1] + w[h][3];
-                }
-                if constexpr (VB > 0) {
-                    if (masked)
-                        output_tile<D, VB, true>(vpart, lane, w, acc);
-                    else
-                        output_tile<D, VB, false>(vpart, lane, w, acc);
-                } else {
-                    switch (a.pg.vb) {
+            for (int h = 0; h < 2; ++h) {
+                l[0] += w[h][0] + w[h][2];
+                l[1] += w[h][1] + w[h][3];
+            }
+            if constexpr (VB > 0) {
+                if (masked)
+                    output_tile<D, VB, true>(vpart, lane, w, acc);
+                else
+                    output_tile<D, VB, false>(vpart, lane, w, acc);
+            } else {
+                switch (a.pg.vb) {
 #define QG_OUTPUT(B)                                               \
     case B:                                                        \
         if (masked)                                                \
@@ -1051,14 +1028,13 @@ __global__ void __launch_bounds__(AttCfg<D>::T, 1) kv_attend_kernel(KvAttend a) 
         else                                                       \
             output_tile<D, B, false>(vpart, lane, w, acc);     \
         break;
-                        QG_OUTPUT(2)
-                        QG_OUTPUT(3)
-                        QG_OUTPUT(4)
-                        QG_OUTPUT(5)
-                        QG_OUTPUT(6)
-                        QG_OUTPUT(8)
+                    QG_OUTPUT(2)
+                    QG_OUTPUT(3)
+                    QG_OUTPUT(4)
+                    QG_OUTPUT(5)
+                    QG_OUTPUT(6)
+                    QG_OUTPUT(8)
 #undef QG_OUTPUT
-                    }
                 }
             }
             __syncwarp();

@@ -3,6 +3,9 @@ attention (tests/kv_reference.py): append byte for byte over whole pages,
 gather and attend within bounds that count their roundings, at ragged lengths,
 empty rows, odd widths, strided operands and unused slots full of NaN."""
 import math
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -436,6 +439,41 @@ def test_decoding_loop(q):
         check_attention(out[:n].double().cpu().numpy(), lse[:n].double().cpu().numpy(),
                         s.attend(qs[:n], heads, D ** -0.5), F16, D, 50)
     assert a == 50 and b == 9
+
+
+FIRST_IN_CAPTURE = """
+import torch
+import mixed_bitwidth_weight_b200 as q
+i32 = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")
+g = torch.Generator(device="cuda").manual_seed(3)
+cache = q.KVCache.zeros(4, 64, 2, 128, 4, 4)
+batch = q.KVBatch(i32([[2, 0, 3]]), i32([150]), i32([0, 150]))
+one = q.KVBatch(i32([[2, 0, 3]]), i32([150]), i32([0, 1]))
+k, v = (torch.randn(150, 2, 128, generator=g, device="cuda").half() for _ in range(2))
+x = torch.randn(1, 8, 128, generator=g, device="cuda").half()
+out, eager, ws = torch.zeros_like(x), torch.zeros_like(x), q.kv_workspace(cache, 8)
+kb, vb = torch.zeros_like(k), torch.zeros_like(v)
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    q.qgemm_kv_append(k, v, cache, batch)
+    q.qgemm_kv_gather(cache, batch, kb, vb)
+    q.qgemm_kv_attend(x, cache, one, out, ws)
+graph.replay()
+torch.cuda.synchronize()
+q.qgemm_kv_attend(x, cache, one, eager, ws)
+assert torch.equal(out, eager) and out.abs().sum() > 0
+assert (kb - k).abs().max() < 1.0 and (vb - v).abs().max() < 1.0
+assert q.qgemm_device_error() == 0
+print("captured first")
+"""
+
+
+def test_first_calls_of_a_process_inside_a_capture():
+    """No call has to come before a capture: a fresh process's first ones are captured, then replayed."""
+    r = subprocess.run([sys.executable, "-c", FIRST_IN_CAPTURE], capture_output=True, text=True, timeout=300,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.returncode == 0 and "captured first" in r.stdout, r.stderr[-2000:]
 
 
 def test_two_streams_with_their_own_workspaces(q):
