@@ -33,8 +33,8 @@
 // schedulers, m16n8k16 takes 8.4 cycles, integer and fp16 instructions 2 each, and
 // they overlap little (one with four ANDs and four fp16 adds: 17.7 cycles of 24.4):
 // 300 cycles a tile and SM against the 200 that its 4608 bytes take from HBM.
-// 524288 tokens x 8 heads x 128: 4/4 bits 165 us (3.6 TB/s, 55% of measured HBM), 6/4
-// bits (393216 tokens) 162 us (3.4 TB/s), 8/8 bits (262144) 96-105 us (5.4-5.9 TB/s).
+// 524288 tokens x 8 heads x 128: 4/4 bits 168 us (3.6 TB/s, 55% of measured HBM), 6/4
+// bits (393216 tokens) 158 us (3.5 TB/s), 8/8 bits (262144) 96-105 us (5.4-5.9 TB/s).
 //
 // Work: the (sequence, head, 8 rows, 32-token tile) space is cut into equal runs per
 // CTA and per warp, whatever the lengths (all read on the device).  A warp walks its

@@ -145,7 +145,7 @@ QG_DEV bool kv_block(const KvBatch& bt, int number, int lane, KvBlock& k) {
 // stored in the widest pieces that a token owns (16 bytes of K, 8 of V at 128
 // dims and 4 bits; eight neighbouring tokens fill whole sectors).
 // Bound by instructions (about 25 cycles a value and lane), not by HBM: 32768 tokens of 8 heads
-// of 128 at 4 bits 65 us, 172 MB read and written (2.6 TB/s); a warp per vector took 280 us.
+// of 128 at 4 bits 70 us, 172 MB read and written (2.5 TB/s).
 
 // bits [at, at + b) of a bit string in 32-bit words
 template <int NW>
