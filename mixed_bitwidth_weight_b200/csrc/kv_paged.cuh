@@ -145,9 +145,9 @@ QG_DEV bool kv_block(const KvBatch& bt, int number, int lane, KvBlock& k) {
 // stored in the widest pieces that a token owns (16 bytes of K, 8 of V at 128
 // dims and 4 bits; eight neighbouring tokens fill whole sectors).
 // Bound by instructions (about 25 cycles a value and lane), not by HBM: 32768 tokens of 8 heads
-// of 128 at 4 bits 70 us, 172 MB read and written (2.5 TB/s).
+// of 128 at 4 bits 68 us, 172 MB read and written (2.5 TB/s).
 
-// bits [at, at + b) of a bit string in 32-bit words
+// bits [at, at + b) of a bit string in 32-bit words, `at` constant after unrolling
 template <int NW>
 QG_DEV void put_bits(uint32_t (&w)[NW], int at, int b, uint32_t v) {
     w[at >> 5] |= v << (at & 31);
@@ -175,8 +175,9 @@ QG_DEV void put_token(uint8_t* part, int t, int lane, bool mine, float (&x)[D / 
     constexpr int G = D / 32, z = 1 << (B - 1);
     constexpr int half = D * B / 16, C = half % 16 == 0 ? 16 : half % 8 == 0 ? 8 : 4;
     const int j = lane & 3, tt = t >> 3;
+    constexpr int N = B == 2 ? 8 : B <= 5 ? 4 : 2;  // codes whose bits a float holds exactly
     __half sh[G];
-    uint32_t code[G][8];
+    float code[G][8];
 #pragma unroll
     for (int g = 0; g < G; ++g) {
         float amax = 0.f;
@@ -188,13 +189,23 @@ QG_DEV void put_token(uint8_t* part, int t, int lane, bool mine, float (&x)[D / 
         const float s = __half2float(sh[g]);
         const float inv = s == 0.f ? 0.f : __frcp_rn(s);  // the zero point everywhere where s is 0
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            // clamped first (whole bounds: the same as after), then rounded to nearest even by the
-            // addition of 1.5 2^23, whose low bits are then the integer
-            const float q = fminf(fmaxf(__fmul_rn(x[g][i], inv), (float)(-z)), (float)(z - 1));
-            code[g][i] = __float_as_uint(__fadd_rn(q, 12582912.f + (float)z)) & 0xffffu;
-        }
+        for (int i = 0; i < 8; ++i) code[g][i] = __fmul_rn(x[g][i], inv);
+        // A normal scale is at least (1 - 2^-11) max / (z - 1): |u / s| <= (z - 1) (1 + 2^-10) rounds to
+        // z - 1 at most.  Others are clamped (before rounding: the bounds are whole, so it is the same).
+        if (!(s >= 6.103515625e-5f && s <= 65504.f))
+#pragma unroll
+            for (int i = 0; i < 8; ++i) code[g][i] = fminf(fmaxf(code[g][i], (float)(-z)), (float)(z - 1));
+        // rounded to nearest even by adding 1.5 2^23; from here whole numbers 0 .. 2 z - 1
+#pragma unroll
+        for (int i = 0; i < 8; ++i) code[g][i] = __fsub_rn(__fadd_rn(code[g][i], 12582912.f + (float)z), 12582912.f);
     }
+    // N codes as one number: exact fused multiply-adds, then the bits of 2^23 + it
+    auto joined = [&](auto&& at) {
+        float v = at(N - 1);
+#pragma unroll
+        for (int i = N - 2; i >= 0; --i) v = fmaf(v, (float)(1 << B), at(i));
+        return __float_as_uint(v + 8388608.f) & 0x7fffffu;
+    };
     if (!mine) return;
     if constexpr (KEY) {
         constexpr int PB = G * B;  // the lane's units of all groups
@@ -202,7 +213,9 @@ QG_DEV void put_token(uint8_t* part, int t, int lane, bool mine, float (&x)[D / 
 #pragma unroll
         for (int g = 0; g < G; ++g)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) put_bits(w, g * 8 * B + i * B, B, code[g][B >= 5 ? kv_wide(i) : i]);
+            for (int i = 0; i < 8; i += N)
+                put_bits(w, g * 8 * B + i * B, N * B,
+                         joined([&](int k) { return code[g][B >= 5 ? kv_wide(i + k) : i + k]; }));
         put_stream<PB, C>(part, lane, tt * PB, w);
     } else {
         constexpr int PB = D / 64 * B;
@@ -213,8 +226,9 @@ QG_DEV void put_token(uint8_t* part, int t, int lane, bool mine, float (&x)[D / 
 #pragma unroll
             for (int h = 0; h < D / 64; ++h)
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    put_bits(w, h * 8 * B + i * B, B, code[2 * h + (i >> 2)][4 * e + (i & 3)]);
+                for (int i = 0; i < 8; i += N)
+                    put_bits(w, h * 8 * B + i * B, N * B,
+                             joined([&](int k) { return code[2 * h + ((i + k) >> 2)][4 * e + ((i + k) & 3)]; }));
             put_stream<PB, C>(part, 4 * (2 * j + e) + jt, (2 * tt + u) * PB, w);
         }
     }

@@ -125,6 +125,25 @@ def test_append_and_gather_every_width(q, D, kb):
             check_rotated_back(got.double().cpu().numpy().reshape(-1, D), u, dtype)
 
 
+@pytest.mark.parametrize("b", [2, 3, 4, 5, 6, 8])
+def test_append_scales_from_zero_to_infinity(q, b):
+    """Token i's values lie about 2^(i - 26): scales of 0, subnormal and normal ones, and infinity, byte for byte."""
+    rng = np.random.default_rng(40 + b)
+    heads, n, D = 2, 42, 128
+    s = problem(rng, [n], [n], heads, D, b, b, 64)
+    cache, batch = to_gpu(q, s, heads)
+    size = 2.0 ** (np.arange(n) - 26.0)[:, None, None]
+    k, v = (np.clip(rng.uniform(-1, 1, (n, heads, D)) * size, -65504, 65504).astype(np.float16) for _ in range(2))
+    k[7] = 0
+    v[-1, :, ::2], v[-1, :, 1::2] = 65504, -65504                  # one rotated value of 128 x 65504, the others 0
+    with np.errstate(over="ignore", invalid="ignore"):
+        s.append(k, v)
+        kinds = R.codes_of(np.concatenate([k, v]).reshape(-1, D), b)[1].view(np.float16).astype(np.float64)
+    assert (kinds == 0).any() and ((kinds > 0) & (kinds < 2.0 ** -14)).any() and np.isinf(kinds).any()
+    q.qgemm_kv_append(torch.as_tensor(k).cuda(), torch.as_tensor(v).cuda(), cache, batch)
+    assert np.array_equal(cache.pages.view(torch.uint8).cpu().numpy(), s.pages)
+
+
 def check_rotated_back(got, u, dtype):
     """v = H u / D: each of log2 D single-precision stages rounds by at most U32 of sums no larger than
     sum |u|, and the result is rounded once to dtype (fp16's step is 2^-24 below 2^-14)."""
