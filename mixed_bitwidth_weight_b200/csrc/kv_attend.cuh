@@ -66,7 +66,8 @@ constexpr int kAttMaxStages = 8;
 constexpr int kAttLowest = -14;       // V scales below 2^-13 count as if they were that
 constexpr float kAttNone = -3.4e38f;  // the weights' offset before any token: below every finite score
 
-template <int D>
+// KB, VB as in the kernel: known widths, or 0.
+template <int D, int KB = 0, int VB = 0>
 struct AttCfg {
     static constexpr int W = D <= 64 ? 12 : 8;   // warps: 168 registers a thread with 12, 255 with 8
     static constexpr int T = 32 * W;
@@ -77,8 +78,10 @@ struct AttCfg {
     static constexpr int SlotBytes = SlotFloats * 4;
     static constexpr int GSlot = RB * D + 2 * RB;     // floats of a global slot
     // an item's rotated query: [g][hi, lo][lane] 16 bytes, then zq [g][8], f [8];
-    // QN of them are shared by the CTA's warps
-    static constexpr int QN = D <= 128 ? 6 : 4;
+    // QN of them are shared by the CTA's warps.  256 dims at 8/8 bits leave room for 2: a ring of one
+    // record of 17408 bytes for each of eight warps (65536 tokens x 8 heads 78.5 us, 3.6 TB/s; seven
+    // warps beside 4 areas 85)
+    static constexpr int QN = D <= 128 ? 6 : KB + VB == 16 ? 2 : 4;
     static constexpr int QZero = G * 256, QFactor = QZero + G * 8;
     static constexpr int QFloats = QFactor + 8, QBytes = QFloats * 4;
     // shared memory: slots, query areas, barriers, fragments, prefix sums, rings
@@ -91,6 +94,10 @@ struct AttCfg {
     // the join's weights and row buffer lie over the query areas
     static constexpr int MaxCtas = 160;
     static_assert(QN * QBytes >= (RB * MaxCtas + RB * D + 2 * RB * 2 * W) * 4, "join buffers");
+    static constexpr int MaxShared = 226 * 1024;  // 227 KB a CTA, some of it static
+    static constexpr int RingRoom = (MaxShared - RingAt) / W / 128 * 128;
+    static constexpr int WidestRecord = 4 * D * (KB > 0 ? KB + VB + 1 : 8 + 6 + 1);  // 8/8 is always known
+    static_assert(RingRoom >= WidestRecord && RingRoom >= SlotBytes, "a ring holds a record of any width, or a slot");
 };
 
 // a slot's fragment: tiles [a, b) of the item whose first tile is number `item`
@@ -732,12 +739,12 @@ QG_DEV void store_row(const KvAttend& a, float (&o)[D / 32], float m, float l, i
 // work one run of instructions that hides the softmax's latency behind the codes' masks
 // (131072 tokens at 4 bits: 8% faster); they are built for 4/4 and 8/8.
 template <int D, int KB, int VB>
-__global__ void __launch_bounds__(AttCfg<D>::T, 1) kv_attend_kernel(KvAttend a) {
+__global__ void __launch_bounds__(AttCfg<D, KB, VB>::T, 1) kv_attend_kernel(KvAttend a) {
     if constexpr (KB > 0) {
         a.pg.kb = KB;
         a.pg.vb = VB;
     }
-    using C = AttCfg<D>;
+    using C = AttCfg<D, KB, VB>;
     constexpr int W = C::W, G = C::G, RB = C::RB, E = D / 32, T = C::T;
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ long long sh_total[W];

@@ -952,16 +952,14 @@ size_t attend_ws_bytes(int D, int sms) {
 
 template <int D, int KB, int VB>
 int launch_attend(KvAttend a, DeviceInfo* dev, bool* attr, cudaStream_t s) {
-    using C = AttCfg<D>;
-    constexpr size_t most = 226 * 1024;  // 227 KB a CTA, some of it static
-    // the ring's stages are whole records; at the end it also takes a fragment
-    const size_t rec = (size_t)4 * D * (a.pg.kb + a.pg.vb + 1), room = (most - C::RingAt) / C::W / 128 * 128;
-    a.stages = (int)std::min<size_t>(kAttMaxStages, room / rec);
-    a.ring_bytes = (int)((std::max(a.stages * rec, (size_t)C::SlotBytes) + 127) / 128 * 128);
-    if (a.stages < 1 || (size_t)a.ring_bytes > room) return QGEMM_ERR_UNSUPPORTED;
+    using C = AttCfg<D, KB, VB>;
+    // the ring's stages are whole records (one at least, see AttCfg); at the end it also takes a fragment
+    const int rec = 4 * D * (a.pg.kb + a.pg.vb + 1);
+    a.stages = std::min(kAttMaxStages, C::RingRoom / rec);
+    a.ring_bytes = (std::max(a.stages * rec, C::SlotBytes) + 127) / 128 * 128;
     if (!*attr) {  // a per-device setting
         if (cudaFuncSetAttribute(kv_attend_kernel<D, KB, VB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)most) != cudaSuccess) {
+                                 C::MaxShared) != cudaSuccess) {
             cudaGetLastError();
             return QGEMM_ERR_CUDA;
         }
