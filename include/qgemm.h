@@ -301,7 +301,9 @@ int qgemm_kv_gather(const qgemm_kv_cache* cache, const qgemm_kv_batch* batch, in
  * h / (q_heads / kv_heads).
  *   out = sum_t softmax(scale q . k'_t) v'_t,  lse = ln sum_t exp(scale q . k'_t)
  * with k', v' the values gather gives before rounding.  A row that sees nothing
- * gives zeros and -inf.
+ * gives zeros and -inf; one that sees a token with an infinite or NaN scale (of an
+ * infinite input, say) gives nothing finite, however small that token's weight
+ * (its lse: where the scale is the key's).
  *   d_q, d_out [num_rows][q_heads][D] of `dtype`; q_heads a multiple of kv_heads;
  *   d_lse      optional fp32 [num_rows][q_heads];
  *   d_ws       qgemm_kv_attend_workspace_bytes(cache, q_heads) bytes, zero-filled

@@ -580,10 +580,12 @@ QG_DEV void v_fields(const uint8_t* part, int half, int lane, uint32_t (&f)[D / 
 // acc += (codes of V) x (weights times scales): half a tile.  w[c]: the weight of
 // token 16 half + 8 (c / 2) + r for row 2 j + c % 2.  The product with the
 // group's scale is taken in fp32 and rounded once, to the fp16 of the B operand;
-// movmatrix turns it from [token][row] to [row][token].
+// movmatrix turns it from [token][row] to [row][token].  hidden: bit 4 half + c of a
+// (token, row) that the mask leaves out, whatever its scale holds; a visible token's NaN
+// counts however small its weight.
 template <int D, bool Masked>
 QG_DEV void v_product(const uint8_t* scales, int half, int lane, const uint32_t (&f)[D / 32][2][4],
-                      const float (&w)[4], float (&acc)[D / 16][4]) {
+                      const float (&w)[4], uint32_t hidden, float (&acc)[D / 16][4]) {
     constexpr int G = D / 32;
     const int r = lane >> 2;
     const uint32_t pick = (r & 1) ? 0x7632u : 0x5410u;  // u of token 8 tt + r
@@ -597,7 +599,7 @@ QG_DEV void v_product(const uint8_t* scales, int half, int lane, const uint32_t 
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
             b[c] = w[c] * (c < 2 ? s0 : s1);
-            if constexpr (Masked) b[c] = w[c] == 0.f ? 0.f : b[c];  // whatever the scale it meets
+            if constexpr (Masked) b[c] = hidden >> (4 * half + c) & 1 ? 0.f : b[c];
         }
         const uint32_t b0 = movm_trans(h2_bits(__floats2half2_rn(b[0], b[1])));
         const uint32_t b1 = movm_trans(h2_bits(__floats2half2_rn(b[2], b[3])));
@@ -607,12 +609,12 @@ QG_DEV void v_product(const uint8_t* scales, int half, int lane, const uint32_t 
 }
 
 template <int D, int B, bool Masked>
-QG_DEV void output_tile(const uint8_t* part, int lane, const float (&w)[2][4], float (&acc)[D / 16][4]) {
+QG_DEV void output_tile(const uint8_t* part, int lane, const float (&w)[2][4], uint32_t hidden, float (&acc)[D / 16][4]) {
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
         uint32_t f[D / 32][2][4];
         v_fields<D, B>(part, half, lane, f);
-        v_product<D, Masked>(part + 4 * D * B, half, lane, f, w[half], acc);
+        v_product<D, Masked>(part + 4 * D * B, half, lane, f, w[half], hidden, acc);
     }
 }
 
@@ -960,6 +962,11 @@ __global__ void __launch_bounds__(AttCfg<D, KB, VB>::T, 1) kv_attend_kernel(KvAt
             const bool none = bad >> stage & 1;
             const bool masked = it < u0 || it >= u1 || none;
             int last = kTileTokens;  // last slot that any row sees
+            uint32_t hidden = 0;
+            // A score of a visible token is -inf only where its scale is infinite: the sum it meets is 0 where
+            // append left zero points, give or take a rounding, and 0 x inf is not a number.  (Left at -inf it
+            // would drop the token without a trace.  +inf makes the row NaN by itself.  The check costs 1 to 3%.)
+            const float nan = __uint_as_float(0x7fc00000u);
             if (masked) {
                 const int t_first = t_base + it * kTileTokens;
                 last = none ? -1 : hi_pos - t_first;
@@ -968,8 +975,20 @@ __global__ void __launch_bounds__(AttCfg<D, KB, VB>::T, 1) kv_attend_kernel(KvAt
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
                         const int t = t_first + 16 * h + 8 * (c >> 1) + r8, pos = qpos[c & 1];
-                        if (t > pos || none || (a.window > 0 && t <= pos - a.window)) s[h][c] = -INFINITY;
+                        if (t > pos || none || (a.window > 0 && t <= pos - a.window)) {
+                            s[h][c] = -INFINITY;
+                            hidden |= 1u << (4 * h + c);
+                        } else if (s[h][c] == -INFINITY) {
+                            s[h][c] = nan;
+                        }
                     }
+            } else if (fminf(fminf(fminf(s[0][0], s[0][1]), fminf(s[0][2], s[0][3])),
+                             fminf(fminf(s[1][0], s[1][1]), fminf(s[1][2], s[1][3]))) == -INFINITY) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        if (s[h][c] == -INFINITY) s[h][c] = nan;
             }
             // Weights are 2^(x - mo): at most 2^(10 - ve) when mo is set, and it is moved when one
             // would pass 2^(14 - ve), so that weight times scale (below 2^(ve + 1)) fits fp16.
@@ -1023,17 +1042,17 @@ __global__ void __launch_bounds__(AttCfg<D, KB, VB>::T, 1) kv_attend_kernel(KvAt
             }
             if constexpr (VB > 0) {
                 if (masked)
-                    output_tile<D, VB, true>(vpart, lane, w, acc);
+                    output_tile<D, VB, true>(vpart, lane, w, hidden, acc);
                 else
-                    output_tile<D, VB, false>(vpart, lane, w, acc);
+                    output_tile<D, VB, false>(vpart, lane, w, 0, acc);
             } else {
                 switch (a.pg.vb) {
 #define QG_OUTPUT(B)                                               \
     case B:                                                        \
         if (masked)                                                \
-            output_tile<D, B, true>(vpart, lane, w, acc);      \
+            output_tile<D, B, true>(vpart, lane, w, hidden, acc);  \
         else                                                       \
-            output_tile<D, B, false>(vpart, lane, w, acc);     \
+            output_tile<D, B, false>(vpart, lane, w, 0, acc);      \
         break;
                     QG_OUTPUT(2)
                     QG_OUTPUT(3)
