@@ -17,6 +17,7 @@ Names follow the C entry points: ``qgemm_pack``, ``qgemm_dequant``, ``qgemm``,
 from __future__ import annotations
 
 import ctypes
+import operator
 import os
 
 import numpy as np
@@ -360,8 +361,19 @@ def qgemm_kv_dequantize(codes, scales, bits, v, stream=None):
 
 # ---------------------------------------------------------- paged KV cache
 
+def _c_int(v, name):
+    """A whole number of the C interface's int (ctypes would keep the low 32 bits of a larger one)."""
+    v = operator.index(v)
+    if not -(1 << 31) <= v < 1 << 31:
+        raise ValueError(f"{name} = {v} does not fit 32 bits")
+    return v
+
+
 def qgemm_kv_page_words(kv_heads: int, head_dim: int, k_bits: int, v_bits: int, page_size: int) -> int:
     """32-bit words of one page of a paged KV cache (see include/qgemm.h)."""
+    for v, name in ((kv_heads, "kv_heads"), (head_dim, "head_dim"), (k_bits, "k_bits"), (v_bits, "v_bits"),
+                    (page_size, "page_size")):
+        _c_int(v, name)
     return _ok(_lib.qgemm_kv_page_words(kv_heads, head_dim, k_bits, v_bits, page_size), "qgemm_kv_page_words")
 
 
@@ -470,7 +482,7 @@ def _kv_move(fn, where, cache, batch, k, v, stream):
     H, D = cache.kv_heads, cache.head_dim
     kp, krs, khs = _kv_rows(k, "k", H, D, k.dtype, dev)
     vp, vrs, vhs = _kv_rows(v, "v", H, D, k.dtype, dev)
-    T = k.shape[0]
+    T = _c_int(k.shape[0], "rows")
     if v.shape[0] != T:
         _shape_error(f"k has {T} rows, v has {v.shape[0]}")
     _ok(fn(cache._ref, batch._ref, T, kp, krs, khs, vp, vrs, vhs, dt, st), where)
@@ -499,6 +511,7 @@ def qgemm_kv_attend(q, cache, batch, out, ws, scale=None, window=0, lse=None, st
     if q.dim() != 3:
         _shape_error("q must be [rows, q_heads, D]")
     T, Hq, D = q.shape
+    _c_int(T, "rows")
     if Hq == 0 or Hq % cache.kv_heads:
         _shape_error(f"q_heads = {Hq} is not a multiple of kv_heads = {cache.kv_heads}")
     qp, qrs, qhs = _kv_rows(q, "q", Hq, cache.head_dim, q.dtype, dev)
@@ -515,14 +528,14 @@ def qgemm_kv_attend(q, cache, batch, out, ws, scale=None, window=0, lse=None, st
     if ws.dtype is not torch.uint8 or ws.get_device() != dev or not ws.is_contiguous():
         raise TypeError(f"ws must be a contiguous uint8 tensor on cuda:{dev}")
     _ok(_lib.qgemm_kv_attend(cache._ref, batch._ref, T, qp, qrs, qhs, dt, Hq, D ** -0.5 if scale is None else scale,
-                             window, op, ors, ohs, lp, ws.data_ptr(), ws.numel(), st), "qgemm_kv_attend")
+                             _c_int(window, "window"), op, ors, ohs, lp, ws.data_ptr(), ws.numel(), st), "qgemm_kv_attend")
     return out
 
 
 def kv_workspace(cache, q_heads: int):
     """A zero-filled workspace of the size qgemm_kv_attend needs."""
     import torch
-    n = int(_lib.qgemm_kv_attend_workspace_bytes(cache._ref, int(q_heads)))
+    n = int(_lib.qgemm_kv_attend_workspace_bytes(cache._ref, _c_int(int(q_heads), "q_heads")))
     if n == 0:
         _shape_error(f"q_heads = {q_heads} is not a multiple of kv_heads = {cache.kv_heads}")
     return torch.zeros(n, dtype=torch.uint8, device=f"cuda:{cache.device_index}")
