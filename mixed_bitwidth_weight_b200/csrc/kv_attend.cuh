@@ -618,20 +618,22 @@ QG_DEV void output_tile(const uint8_t* part, int lane, const float (&w)[2][4], u
     }
 }
 
-// largest V scale among this lane's share of the tile's, up to token slot `last`
-// (slots behind the last visible token may hold anything)
-template <int D>
-QG_DEV __half2 v_scale_max(const uint8_t* part, int vb, int lane, int last) {
+// largest V scale among this lane's share of the tile's, of the token slots in `seen` (what the
+// others hold shall not cost the visible ones their bits); Finite: of the finite ones
+template <int D, bool Finite>
+QG_DEV __half2 v_scale_max(const uint8_t* part, int vb, int lane, uint32_t seen) {
     constexpr int G = D / 32, N = D / 64;  // words of a lane, [j][g][tt] in all
     const uint32_t* w = reinterpret_cast<const uint32_t*>(part + 4 * D * vb) + N * lane;
     __half2 m = bits_h2(0);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
         uint32_t u = w[i];
-        if (last < kTileTokens - 1) {
+        if (seen != 0xffffffffu) {
             const int at = N * lane + i, t = 8 * (at & 3) + 2 * (at / (4 * G));
-            u &= t + 1 <= last ? 0xffffffffu : t <= last ? 0xffffu : 0u;
+            u &= (seen >> t & 1u ? 0xffffu : 0u) | (seen >> t & 2u ? 0xffff0000u : 0u);
         }
+        if constexpr (Finite)
+            u &= ((u & 0x7c00u) != 0x7c00u ? 0xffffu : 0u) | ((u & 0x7c000000u) != 0x7c000000u ? 0xffff0000u : 0u);
         m = __hmax2(m, bits_h2(u));
     }
     return m;
@@ -961,7 +963,7 @@ __global__ void __launch_bounds__(AttCfg<D, KB, VB>::T, 1) kv_attend_kernel(KvAt
             // a tile without a page shows nothing
             const bool none = bad >> stage & 1;
             const bool masked = it < u0 || it >= u1 || none;
-            int last = kTileTokens;  // last slot that any row sees
+            uint32_t seen = 0xffffffffu;  // slots that any row sees
             uint32_t hidden = 0;
             // A score of a visible token is -inf only where its scale is infinite: the sum it meets is 0 where
             // append left zero points, give or take a rounding, and 0 x inf is not a number.  (Left at -inf it
@@ -969,7 +971,9 @@ __global__ void __launch_bounds__(AttCfg<D, KB, VB>::T, 1) kv_attend_kernel(KvAt
             const float nan = __uint_as_float(0x7fc00000u);
             if (masked) {
                 const int t_first = t_base + it * kTileTokens;
-                last = none ? -1 : hi_pos - t_first;
+                const int last = none ? -1 : min(hi_pos - t_first, kTileTokens - 1);
+                const int first = a.window > 0 ? max(lo_pos - a.window + 1 - t_first, 0) : 0;
+                seen = first > last ? 0u : 0xffffffffu >> (kTileTokens - 1 - last) & 0xffffffffu << first;
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -1009,10 +1013,14 @@ __global__ void __launch_bounds__(AttCfg<D, KB, VB>::T, 1) kv_attend_kernel(KvAt
                 tm[c] = q.f[c] * fmaxf(fmaxf(s[0][c], s[0][c + 2]), fmaxf(s[1][c], s[1][c + 2]));
                 over |= tm[c] > limit[c];
             }
-            const __half2 vmax = v_scale_max<D>(vpart, a.pg.vb, lane, last);
+            const __half2 vmax = v_scale_max<D, false>(vpart, a.pg.vb, lane, seen);
             over |= !__hblt2(vmax, bits_h2((uint32_t)(16 + ve) * 0x04000400u));  // 2^(ve + 1), infinity for 15
             if (__any_sync(0xffffffffu, over)) {
                 float t = fmaxf(__low2float(vmax), __high2float(vmax));
+                if (t == INFINITY) {  // its rows are NaN whatever the weights' offset
+                    const __half2 f = v_scale_max<D, true>(vpart, a.pg.vb, lane, seen);
+                    t = fmaxf(__low2float(f), __high2float(f));
+                }
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, o));
                 const int vn = min(max((int)(__float_as_uint(t) >> 23) - 127, ve), 15);

@@ -128,3 +128,36 @@ def test_a_vanished_weight_does_not_hide_a_value_that_is_no_number(q, D, b, scal
     nan = torch.isnan(out).all(-1).cpu().numpy()
     assert nan[[0, 1, 4]].all()
     assert torch.isfinite(out[[2, 3]]).all() and torch.isfinite(lse[[2, 3]]).all()
+
+
+@pytest.mark.parametrize("D,b", [(64, 8), (128, 8), (256, 8)])
+@pytest.mark.parametrize("scale", [0x7c00, 0x7bff])
+def test_hidden_values_cost_the_visible_ones_no_bits(q, D, b, scale):  # noqa: F811
+    """Small values next to one of infinite or largest scale, in the same tile, that the window hides: the weights keep
+    the bits that the small ones need. An infinite one that only the last of three rows sees spoils that row alone."""
+    rng = np.random.default_rng(D + scale)
+    heads, G = 2, 4
+    lens, news, window = [200, 150, 93], [1, 1, 3], 40
+    s = problem(rng, lens, news, heads, D, b, b, 64, fill="none")
+    C.centred(rng, s, heads)
+    sv = R.parts(D, b, b)[3]
+    part = s.pages[..., sv:sv + 2 * D].view(np.float16)
+    part[...] = (part.astype(np.float64) * 2.0 ** -9).astype(np.float16)
+    spoil(s, 1, 109, False, scale)           # the row at 149 sees 110 on
+    spoil(s, 2, 92, False, 0x7c00)           # the last row alone
+    spoil(s, 2, 33, False, scale)            # before every row's window
+    spoil(s, 0, 159, False, scale)           # the row at 199 sees 160 on
+    cache, batch = to_gpu(q, s, heads)
+    qs = values(rng, (5, heads * G, D), F16, spread=0.1)
+    out, lse = torch.empty(5, heads * G, D, dtype=F16, device="cuda"), torch.empty(5, heads * G, device="cuda")
+    factor = 0.2 * D ** -0.5
+    q.qgemm_kv_attend(torch.as_tensor(qs).to(F16).cuda(), cache, batch, out, q.kv_workspace(cache, heads * G),
+                      scale=factor, window=window, lse=lse)
+    assert not torch.isfinite(out[4]).any()
+    with np.errstate(invalid="ignore"):
+        r = C.attend_terms(s, qs, heads, factor, window)
+    keep = slice(0, 4)
+    r = {k: v[keep] for k, v in r.items()}
+    got = out.double().cpu().numpy()[keep]
+    # scales of 2^-15 count as 2^-13, so the largest product may be 2^8: twice the bound's share of small ones
+    assert C.output_excess(got, r, torch.finfo(F16).eps, D, 2 * window, 8) <= 1
