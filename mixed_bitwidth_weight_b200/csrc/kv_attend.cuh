@@ -618,23 +618,37 @@ QG_DEV void output_tile(const uint8_t* part, int lane, const float (&w)[2][4], u
     }
 }
 
-// largest V scale among this lane's share of the tile's, of the token slots in `seen` (what the
-// others hold shall not cost the visible ones their bits); Finite: of the finite ones
-template <int D, bool Finite>
-QG_DEV __half2 v_scale_max(const uint8_t* part, int vb, int lane, uint32_t seen) {
+// largest V scale among this lane's share of the tile's, up to token slot `last` (slots behind
+// the last visible token may hold anything)
+template <int D>
+QG_DEV __half2 v_scale_max(const uint8_t* part, int vb, int lane, int last) {
     constexpr int G = D / 32, N = D / 64;  // words of a lane, [j][g][tt] in all
     const uint32_t* w = reinterpret_cast<const uint32_t*>(part + 4 * D * vb) + N * lane;
     __half2 m = bits_h2(0);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
         uint32_t u = w[i];
-        if (seen != 0xffffffffu) {
+        if (last < kTileTokens - 1) {
             const int at = N * lane + i, t = 8 * (at & 3) + 2 * (at / (4 * G));
-            u &= (seen >> t & 1u ? 0xffffu : 0u) | (seen >> t & 2u ? 0xffff0000u : 0u);
+            u &= t + 1 <= last ? 0xffffffffu : t <= last ? 0xffffu : 0u;
         }
-        if constexpr (Finite)
-            u &= ((u & 0x7c00u) != 0x7c00u ? 0xffffu : 0u) | ((u & 0x7c000000u) != 0x7c000000u ? 0xffff0000u : 0u);
         m = __hmax2(m, bits_h2(u));
+    }
+    return m;
+}
+
+// The largest that weights have to fit, among slots first to last: a hidden one shall not cost the
+// visible ones their bits, and an infinite one makes its rows NaN whatever the weights.
+template <int D>
+QG_DEV float v_scale_fit(const uint8_t* part, int vb, int lane, int first, int last) {
+    constexpr int G = D / 32, N = D / 64;
+    const __half* s = reinterpret_cast<const __half*>(part + 4 * D * vb) + 2 * N * lane;
+    float m = 0.f;
+#pragma unroll
+    for (int i = 0; i < 2 * N; ++i) {
+        const int at = N * lane + i / 2, t = 8 * (at & 3) + 2 * (at / (4 * G)) + (i & 1);
+        const float v = __half2float(s[i]);
+        if (t >= first && t <= last && v < INFINITY) m = fmaxf(m, v);
     }
     return m;
 }
@@ -963,17 +977,15 @@ __global__ void __launch_bounds__(AttCfg<D, KB, VB>::T, 1) kv_attend_kernel(KvAt
             // a tile without a page shows nothing
             const bool none = bad >> stage & 1;
             const bool masked = it < u0 || it >= u1 || none;
-            uint32_t seen = 0xffffffffu;  // slots that any row sees
+            int last = kTileTokens;  // last slot that any row sees
             uint32_t hidden = 0;
             // A score of a visible token is -inf only where its scale is infinite: the sum it meets is 0 where
             // append left zero points, give or take a rounding, and 0 x inf is not a number.  (Left at -inf it
-            // would drop the token without a trace.  +inf makes the row NaN by itself.  The check costs 1 to 3%.)
+            // would drop the token without a trace; +inf makes the row NaN by itself.)
             const float nan = __uint_as_float(0x7fc00000u);
             if (masked) {
                 const int t_first = t_base + it * kTileTokens;
-                const int last = none ? -1 : min(hi_pos - t_first, kTileTokens - 1);
-                const int first = a.window > 0 ? max(lo_pos - a.window + 1 - t_first, 0) : 0;
-                seen = first > last ? 0u : 0xffffffffu >> (kTileTokens - 1 - last) & 0xffffffffu << first;
+                last = none ? -1 : hi_pos - t_first;
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -986,17 +998,11 @@ __global__ void __launch_bounds__(AttCfg<D, KB, VB>::T, 1) kv_attend_kernel(KvAt
                             s[h][c] = nan;
                         }
                     }
-            } else if (fminf(fminf(fminf(s[0][0], s[0][1]), fminf(s[0][2], s[0][3])),
-                             fminf(fminf(s[1][0], s[1][1]), fminf(s[1][2], s[1][3]))) == -INFINITY) {
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        if (s[h][c] == -INFINITY) s[h][c] = nan;
             }
             // Weights are 2^(x - mo): at most 2^(10 - ve) when mo is set, and it is moved when one
             // would pass 2^(14 - ve), so that weight times scale (below 2^(ve + 1)) fits fp16.
-            // (The weights are computed before it is known, again if it has to be moved.)
+            // (The weights are computed before it is known, again if it has to be moved, and after the rare
+            // infinite score of a tile seen whole, which takes the same branch: 1% in all, 2% in one of its own.)
             float w[2][4];
             auto weigh = [&] {
 #pragma unroll
@@ -1013,14 +1019,19 @@ __global__ void __launch_bounds__(AttCfg<D, KB, VB>::T, 1) kv_attend_kernel(KvAt
                 tm[c] = q.f[c] * fmaxf(fmaxf(s[0][c], s[0][c + 2]), fmaxf(s[1][c], s[1][c + 2]));
                 over |= tm[c] > limit[c];
             }
-            const __half2 vmax = v_scale_max<D, false>(vpart, a.pg.vb, lane, seen);
+            const __half2 vmax = v_scale_max<D>(vpart, a.pg.vb, lane, last);
             over |= !__hblt2(vmax, bits_h2((uint32_t)(16 + ve) * 0x04000400u));  // 2^(ve + 1), infinity for 15
+            const float lo = fminf(fminf(fminf(s[0][0], s[0][1]), fminf(s[0][2], s[0][3])),
+                                   fminf(fminf(s[1][0], s[1][1]), fminf(s[1][2], s[1][3])));
+            over |= !masked && lo == -INFINITY;
             if (__any_sync(0xffffffffu, over)) {
-                float t = fmaxf(__low2float(vmax), __high2float(vmax));
-                if (t == INFINITY) {  // its rows are NaN whatever the weights' offset
-                    const __half2 f = v_scale_max<D, true>(vpart, a.pg.vb, lane, seen);
-                    t = fmaxf(__low2float(f), __high2float(f));
-                }
+                if (!masked)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) s[h][c] = s[h][c] == -INFINITY ? nan : s[h][c];
+                const int first = a.window > 0 ? lo_pos - a.window + 1 - t_base - it * kTileTokens : 0;
+                float t = v_scale_fit<D>(vpart, a.pg.vb, lane, first, last);
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, o));
                 const int vn = min(max((int)(__float_as_uint(t) >> 23) - 127, ve), 15);
