@@ -310,7 +310,11 @@ int qgemm_kv_gather(const qgemm_kv_cache* cache, const qgemm_kv_batch* batch, in
  *              before its first use and reusable after each completed call; calls
  *              that overlap on the GPU must not share it.
  * The number of tokens and the split over them are read on the device, so a
- * captured call can be replayed with other lengths. */
+ * captured call can be replayed with other lengths.
+ * Made for few new rows a sequence (a token, some drafts): every 8 rows (tokens x
+ * query heads of a KV head) read all that any new row of their sequence sees.  A
+ * prompt of n tokens is attended rightly, at a cost that grows with n^2 x heads,
+ * about twice what its causal half needs, more with a window far shorter than n. */
 size_t qgemm_kv_attend_workspace_bytes(const qgemm_kv_cache* cache, int q_heads);
 int qgemm_kv_attend(const qgemm_kv_cache* cache, const qgemm_kv_batch* batch, int num_rows, const void* d_q, int64_t q_row_stride,
                     int64_t q_head_stride, int dtype, int q_heads, float scale, int window, void* d_out,

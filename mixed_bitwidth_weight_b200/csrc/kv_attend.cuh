@@ -10,11 +10,11 @@
 // Scores, per group g of 32 dims: sum_d (Hq)_d (c - z) on m16n8k16 with the
 // codes as the A operand (16 tokens), 8 query rows as B.  A code's bits, masked
 // out of its word, ARE an fp16 number: the subnormal c 2^-24 (or, i bits further
-// up where it lies, c 2^(i-24); the query carries 2^-i).  So a pair of codes costs
-// one AND.  The accumulators start at -z sum_d (Hq)_d instead of 0, and the
-// token's scale multiplies the group's sum in fp32.  The rotated query is held as
-// two fp16 parts (22 bits, scaled by the row's power of two), each times the exact
-// codes.
+// up where it lies, c 2^(i-24); the query carries 2^-i).  So a pair of codes costs one
+// AND, and up to 5 bits one exact multiplication more (kNorm).  The accumulators start
+// at -z sum_d (Hq)_d instead of 0, and the token's scale multiplies the group's sum in
+// fp32.  The rotated query is held as two fp16 parts (22 bits, scaled by the row's power
+// of two), each times the exact codes.
 // Output: A = codes of V (16 dims x 16 tokens), c - z by one exact fused
 // multiply-add a pair (starting at -z sum p would lose the sum of many tokens to
 // cancellation), B = p s_g.  p, s and their product are fp32, the product is
@@ -29,21 +29,26 @@
 // and 8 query rows fill 1/16 of its M.
 //
 // What bounds it: instructions, not HBM, below 8 bits.  A tile of 32 tokens of 128
-// dims at 4 bits takes about 540 instructions of a warp.  Measured on the four
+// dims at 4 bits takes 663 instructions of a warp: 48 mma, 106 logic, 128 fp16 arithmetic
+// and 32 conversions, 56 byte permutes, 74 fp32.  Measured on the four
 // schedulers, m16n8k16 takes 8.4 cycles, integer and fp16 instructions 2 each, and
 // they overlap little (one with four ANDs and four fp16 adds: 17.7 cycles of 24.4):
-// 300 cycles a tile and SM against the 200 that its 4608 bytes take from HBM.
-// 524288 tokens x 8 heads x 128: 4/4 bits 168 us (3.6 TB/s, 55% of measured HBM), 6/4
-// bits (393216 tokens) 158 us (3.5 TB/s), 8/8 bits (262144) 96-105 us (5.4-5.9 TB/s).
+// 340 cycles a tile and SM against the 205 that its 4608 bytes take from HBM.
+// 8 heads x 128, 64 query heads: 4/4 bits, 524288 tokens 176 us (3.4 TB/s, 53% of measured
+// HBM); 8/8 bits, 262144 tokens 99 us (5.8 TB/s, 89%).
 //
 // Work: the (sequence, head, 8 rows, 32-token tile) space is cut into equal runs per
-// CTA and per warp, whatever the lengths (all read on the device).  A warp walks its
+// CTA and per warp, whatever the lengths (all read on the device).  Every 8 rows walk all tiles
+// that any new row of their sequence sees, and unpack them again.  A warp walks its
 // run with a ring of bulk copies (one record each; a separate feeding warp was slower,
 // per-lane asynchronous copies too); what it has of an item is joined in shared memory
 // per CTA, and across CTAs by the last one to arrive, in a fixed order, so results
 // repeat bit for bit.  Eight warps of up to 255 registers: twelve of 168 gained 4% on
 // long sequences and lost 15% on short ones, except at 64 dims.  Scan, seek, first copies
-// and join are about 8 us whatever the length.
+// and join are about 8 us whatever the length.  At 256 dims join slots and query areas
+// leave a ring of one record a warp for 30 of the 36 pairs of widths (more where they sum
+// to 6 bits or fewer), so a warp's copies and its arithmetic do not overlap, and ptxas
+// spills: 96 to 128 bytes of stack a thread.
 #pragma once
 
 #include "kv_paged.cuh"
@@ -754,8 +759,12 @@ QG_DEV void store_row(const KvAttend& a, float (&o)[D / 32], float m, float l, i
 }
 
 // KB, VB: the widths, or 0 where they are read from `a`.  Known widths make a tile's
-// work one run of instructions that hides the softmax's latency behind the codes' masks
-// (131072 tokens at 4 bits: 8% faster); they are built for 4/4 and 8/8.
+// work one run of instructions that hides the softmax's latency behind the codes' masks;
+// they are built for 4/4 and 8/8.  Known against read, us (8 KV heads, 64 query heads; one long
+// sequence, and 64 of 200 to 4096 tokens):
+//   64 dims, 524288 tokens: 4/4 111 / 114, 50 / 52; 8/8 107 / 117, 55 / 60;
+//   128 dims, 262144 tokens: 4/4 98 / 107, 76 / 86; 8/8 100 / 109, 78 / 92;
+//   256 dims, 131072 tokens: 4/4 112 / 119, 140 / 161.
 template <int D, int KB, int VB>
 __global__ void __launch_bounds__(AttCfg<D, KB, VB>::T, 1) kv_attend_kernel(KvAttend a) {
     if constexpr (KB > 0) {
